@@ -12,6 +12,18 @@ load, importing the functions below raises.
     gdn2_chunk_bwd(q, k, v, log_alpha, b, w, dO, S0=None, dS_T=None, ...)
         -> (dq, dk, dv, dlog_alpha, db, dw, dS0)
     gdn2_device_status(stream=None) -> int   (device-side error bits, read and cleared)
+
+Around the state pool, for serving (states in 8 bits: int8 or float8_e4m3fn codes and one fp32
+scale per key row; drafted tokens verified, and the states rolled back to the accepted ones):
+
+    gdn2_state_store(S, codes, scales, slots=None) -> (codes, scales)
+    gdn2_state_load(codes, scales, slots=None, ...) -> S
+    gdn2_decode_multi_q8(q, k, v, log_alpha, b, w, codes, scales, slots=None, slots_out=None, ...)
+        -> (o, code_steps, scale_steps)                        (the pool updated in place)
+    gdn2_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, ...)
+        -> (n_accepted, tokens)
+    gdn2_state_commit(S_steps, index, S_pool, slots=None)
+    gdn2_state_commit_q8(code_steps, scale_steps, index, codes, scales, slots=None)
 """
 from __future__ import annotations
 
@@ -25,11 +37,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgdn2.so")
 
 GDN2_F32, GDN2_BF16 = 0, 1
+GDN2_Q8_INT8, GDN2_Q8_E4M3 = 0, 1  # 8-bit state formats
+GDN2_VERIFY_MAX_DRAFTS, GDN2_VERIFY_MAX_VOCAB = 31, 4194304  # limits of gdn2_verify_drafts (gdn2.h)
 GDN2_DECODE_MAX_TOKENS = 8  # tokens per sequence in one gdn2_decode_multi call (gdn2.h)
 STATUS = {0: "GDN2_OK", 1: "GDN2_ERR_INVALID_ARG", 2: "GDN2_ERR_UNSUPPORTED", 3: "GDN2_ERR_CUDA"}
 ABI_FUNCTIONS = ("gdn2_chunk_fwd_workspace_size", "gdn2_chunk_fwd", "gdn2_chunk_fwd_prologue",
                  "gdn2_chunk_fwd_noalloc", "gdn2_decode_step", "gdn2_decode_multi",
                  "gdn2_decode_multi_prologue", "gdn2_chunk_bwd_workspace_size", "gdn2_chunk_bwd",
+                 "gdn2_state_store", "gdn2_state_load", "gdn2_decode_multi_q8", "gdn2_decode_multi_q8_prologue",
+                 "gdn2_verify_drafts", "gdn2_state_commit", "gdn2_state_commit_q8",
                  "gdn2_device_status", "gdn2_testing_set_wait_limit", "gdn2_last_error_string",
                  "gdn2_version")
 # bits of the device status word (gdn2_device_status)
@@ -80,6 +96,17 @@ def load_library(path: str = LIB_PATH):
     lib.gdn2_chunk_bwd_workspace_size.argtypes = [ctypes.POINTER(Shape)]
     lib.gdn2_chunk_bwd.restype = ctypes.c_int
     lib.gdn2_chunk_bwd.argtypes = [ctypes.POINTER(Shape)] + [vp] * 17 + [vp, sz, vp]
+    ci = ctypes.c_int
+    for name, args in (
+            ("gdn2_state_store", [ci] * 5 + [vp] * 4 + [ci, vp]),
+            ("gdn2_state_load", [ci] * 5 + [vp] * 2 + [ci] + [vp] * 3),
+            ("gdn2_decode_multi_q8", [ctypes.POINTER(Shape), ci, ci] + [vp] * 10 + [ci] + [vp] * 4),
+            ("gdn2_decode_multi_q8_prologue", [ctypes.POINTER(Shape), ci, ci] + [vp] * 10 + [ci] + [vp] * 4),
+            ("gdn2_verify_drafts", [ci] * 4 + [vp] * 9),
+            ("gdn2_state_commit", [ci] * 5 + [vp] * 4 + [ci, vp]),
+            ("gdn2_state_commit_q8", [ci] * 5 + [vp] * 6 + [ci, vp])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
     lib.gdn2_device_status.restype = ctypes.c_int
     lib.gdn2_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), vp]
     lib.gdn2_testing_set_wait_limit.restype = None
@@ -117,6 +144,9 @@ def _expect(name, t, shape, dtype=None, device=None, optional=False):
     """Argument check before any launch: the kernels take raw pointers and read each tensor
     densely at the shape the call implies, so a tensor of another shape, strided, on the
     host or of another type would be read out of bounds or misread."""
+    if (t.__class__ is torch.Tensor and t.is_cuda and t.shape == shape and t.is_contiguous()
+            and dtype in (None, t.dtype) and device in (None, t.device)):
+        return  # the usual case, in one step: the checks below only say what is wrong
     if t is None:
         if optional:
             return
@@ -348,6 +378,201 @@ def gdn2_chunk(q, k, v, log_alpha, b, w, S0=None, cu_seqlens=None, n_seq=None):
     takes the gradients of every input (and of S0) from gdn2_chunk_bwd, cast to each
     input's dtype. Same shapes and rules as gdn2_chunk_fwd."""
     return _ChunkFn.apply(q, k, v, log_alpha, b, w, S0, cu_seqlens, n_seq)
+
+
+# ---------------------------------------------------------------- around the state pool
+
+_Q8_FORMAT = {torch.int8: GDN2_Q8_INT8, torch.float8_e4m3fn: GDN2_Q8_E4M3}
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device), _on(stream):
+        yield
+
+
+def _at(device, stream):
+    """The call's device made current for its launch, and its outputs allocated on its stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return _switched(device, stream)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device, stream):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _expect_pool(codes, scales):
+    """Codes [n_slots, Hv, dk, dv] and their scales [n_slots, Hv, dk] of an 8-bit pool; returns the
+    format and the pool's sizes."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() != 4:
+        raise ValueError("codes must be a CUDA tensor [n_slots, Hv, dk, dv]")
+    if codes.dtype not in _Q8_FORMAT:
+        raise TypeError(f"codes is {codes.dtype}, expected torch.int8 or torch.float8_e4m3fn")
+    _expect("codes", codes, codes.shape, None, codes.device)
+    _expect("scales", scales, codes.shape[:3], torch.float32, codes.device)
+    return _Q8_FORMAT[codes.dtype], codes.shape
+
+
+def gdn2_state_store(S, codes, scales, slots=None, stream=None):
+    """Quantise states into slots of an 8-bit pool.
+
+    S fp32 [N,Hv,dk,dv]; codes int8 or float8_e4m3fn [n_slots,Hv,dk,dv] and scales fp32
+    [n_slots,Hv,dk], written at each sequence's slot; slots int32 [N] (out of range: not stored;
+    no two sequences may share one) or None (slot n). Returns (codes, scales)."""
+    fmt, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
+    dev = codes.device
+    n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else 0
+    _expect("S", S, (n, h_v, dk, dv), torch.float32, dev)
+    _expect("slots", slots, (n,), torch.int32, dev, optional=True)
+    with _at(dev, stream):
+        _check(load_library().gdn2_state_store(n, h_v, dk, dv, fmt, S.data_ptr(), _p(slots), codes.data_ptr(),
+                                               scales.data_ptr(), n_slots, _raw_stream(dev, stream)))
+    return codes, scales
+
+
+def gdn2_state_load(codes, scales, slots=None, n_seq=None, S=None, stream=None):
+    """Read states back from an 8-bit pool, for example as the S0 of a prefill: fp32 [N,Hv,dk,dv].
+    slots int32 [N] (out of range: the zero state) or None (slot n of the first ``n_seq``, by
+    default all, slots). ``S``, if given, is written and returned."""
+    fmt, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
+    dev = codes.device
+    if slots is not None:
+        n = slots.numel() if isinstance(slots, torch.Tensor) else 0
+        _expect("slots", slots, (n,), torch.int32, dev)
+    else:
+        n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else n_slots
+    if n_seq is not None:
+        if slots is not None or S is not None:
+            if int(n_seq) != n:
+                raise ValueError(f"n_seq = {n_seq}, but slots or S has {n} sequences")
+        n = int(n_seq)
+    _expect("S", S, (n, h_v, dk, dv), torch.float32, dev, optional=True)
+    with _at(dev, stream):
+        if S is None:
+            S = torch.empty((n, h_v, dk, dv), dtype=torch.float32, device=dev)
+        _check(load_library().gdn2_state_load(n, h_v, dk, dv, fmt, codes.data_ptr(), scales.data_ptr(), n_slots,
+                                              _p(slots), S.data_ptr(), _raw_stream(dev, stream)))
+    return S
+
+
+def gdn2_decode_multi_q8(q, k, v, log_alpha, b, w, codes, scales, slots=None, slots_out=None, o=None,
+                         code_steps=None, scale_steps=None, want_steps: bool = False, stream=None,
+                         out_dtype=torch.float32, prologue: bool = False):
+    """gdn2_decode_multi on an 8-bit pool: states read as codes, advanced in fp32 and quantised as
+    they are written.
+
+    codes int8 or float8_e4m3fn [n_slots,Hv,dk,dv], scales fp32 [n_slots,Hv,dk]; the tokens, slots
+    and ``prologue`` as for gdn2_decode_multi. slots_out int32 [N]: where each state is written
+    (None: where it was read; out of range: nowhere). Returns (o, code_steps [N,n_tok,Hv,dk,dv],
+    scale_steps [N,n_tok,Hv,dk]), the last two -- the state after each token -- None unless given
+    or wanted."""
+    fmt, (n_slots, p_h, p_dk, p_dv) = _expect_pool(codes, scales)
+    if o is not None:
+        out_dtype = o.dtype
+    N, n_tok = (v.shape[0], v.shape[1]) if isinstance(v, torch.Tensor) and v.dim() == 4 else (0, 0)
+    h_qk, dk, h_v, dv, dev = _expect_tokens(q, k, v, log_alpha, b, w, (N, n_tok), prologue)
+    _expect("codes", codes, (n_slots, h_v, dk, dv), None, dev)
+    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
+    _expect("slots_out", slots_out, (N,), torch.int32, dev, optional=True)
+    _expect("o", o, (N, n_tok, h_v, dv), None, dev, optional=True)
+    _expect("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, dev, optional=True)
+    _expect("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, dev, optional=True)
+    if (code_steps is None) != (scale_steps is None):
+        raise ValueError("code_steps and scale_steps are given together or not at all")
+    shape = Shape(N, N * n_tok, h_qk, h_v, dk, dv, _dtype_code(v.dtype), _dtype_code(out_dtype))
+    with _at(dev, stream):
+        if o is None:
+            o = torch.empty((N, n_tok, h_v, dv), dtype=out_dtype, device=dev)
+        if code_steps is None and want_steps:
+            code_steps = torch.empty((N, n_tok, h_v, dk, dv), dtype=codes.dtype, device=dev)
+            scale_steps = torch.empty((N, n_tok, h_v, dk), dtype=torch.float32, device=dev)
+        lib = load_library()
+        fn = lib.gdn2_decode_multi_q8_prologue if prologue else lib.gdn2_decode_multi_q8
+        _check(fn(ctypes.byref(shape), fmt, n_tok, _p(slots), _p(slots_out), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                  log_alpha.data_ptr(), b.data_ptr(), w.data_ptr(), codes.data_ptr(), scales.data_ptr(), n_slots,
+                  o.data_ptr(), _p(code_steps), _p(scale_steps), _raw_stream(dev, stream)))
+    return o, code_steps, scale_steps
+
+
+def gdn2_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n_drafted=None,
+                       n_accepted=None, tokens=None, stream=None):
+    """Verify drafted tokens against the target's probabilities, from given random numbers.
+
+    target_probs [N,n_draft+1,V] and draft_probs [N,n_draft,V], bf16 or fp32 (draft_probs None:
+    each draft was certain); draft_tokens int32 [N,n_draft]; u_accept fp32 [N,n_draft] and
+    u_sample fp32 [N], uniform in [0, 1); n_drafted int32 [N] (a sequence's own number of drafts;
+    negative = inactive) or None (n_draft each). Returns (n_accepted int32 [N], tokens int32
+    [N,n_draft+1]: the accepted tokens, then the one drawn for the next place, then -1)."""
+    if not isinstance(target_probs, torch.Tensor) or not target_probs.is_cuda or target_probs.dim() != 3:
+        raise ValueError("target_probs must be a CUDA tensor [N, n_draft + 1, V]")
+    N, n1, V = target_probs.shape
+    dt, dev = target_probs.dtype, target_probs.device
+    code = _dtype_code(dt)
+    n = n1 - 1
+    if n < 0:
+        raise ValueError("target_probs has no place for a token: its second size is n_draft + 1")
+    _expect("target_probs", target_probs, (N, n1, V), dt, dev)
+    _expect("draft_probs", draft_probs, (N, n, V), dt, dev, optional=True)
+    _expect("draft_tokens", draft_tokens, (N, n), torch.int32, dev)
+    _expect("u_accept", u_accept, (N, n), torch.float32, dev)
+    _expect("u_sample", u_sample, (N,), torch.float32, dev)
+    _expect("n_drafted", n_drafted, (N,), torch.int32, dev, optional=True)
+    _expect("n_accepted", n_accepted, (N,), torch.int32, dev, optional=True)
+    _expect("tokens", tokens, (N, n1), torch.int32, dev, optional=True)
+    with _at(dev, stream):
+        if n_accepted is None:
+            n_accepted = torch.empty((N,), dtype=torch.int32, device=dev)
+        if tokens is None:
+            tokens = torch.empty((N, n1), dtype=torch.int32, device=dev)
+        _check(load_library().gdn2_verify_drafts(
+            N, n, V, code, target_probs.data_ptr(), _p(draft_probs), draft_tokens.data_ptr(), _p(n_drafted),
+            u_accept.data_ptr(), u_sample.data_ptr(), n_accepted.data_ptr(), tokens.data_ptr(),
+            _raw_stream(dev, stream)))
+    return n_accepted, tokens
+
+
+def gdn2_state_commit(S_steps, index, S_pool, slots=None, stream=None):
+    """Put the state after token index[n] (as gdn2_decode_multi left it in S_steps fp32
+    [N,n_tok,Hv,dk,dv]) back into the sequence's slot of S_pool fp32 [n_slots,Hv,dk,dv]. index
+    int32 [N], for example n_accepted of gdn2_verify_drafts (outside 0..n_tok-1: left as it is);
+    slots as for gdn2_decode_multi. Returns S_pool."""
+    if not isinstance(S_pool, torch.Tensor) or not S_pool.is_cuda or S_pool.dim() != 4:
+        raise ValueError("S_pool must be a CUDA tensor [n_slots, Hv, dk, dv]")
+    n_slots, h_v, dk, dv = S_pool.shape
+    dev = S_pool.device
+    N, n_tok = S_steps.shape[:2] if isinstance(S_steps, torch.Tensor) and S_steps.dim() == 5 else (0, 0)
+    _expect("S_pool", S_pool, (n_slots, h_v, dk, dv), torch.float32, dev)
+    _expect("S_steps", S_steps, (N, n_tok, h_v, dk, dv), torch.float32, dev)
+    _expect("index", index, (N,), torch.int32, dev)
+    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
+    with _at(dev, stream):
+        _check(load_library().gdn2_state_commit(N, h_v, dk, dv, n_tok, S_steps.data_ptr(), index.data_ptr(), _p(slots),
+                                                S_pool.data_ptr(), n_slots, _raw_stream(dev, stream)))
+    return S_pool
+
+
+def gdn2_state_commit_q8(code_steps, scale_steps, index, codes, scales, slots=None, stream=None):
+    """gdn2_state_commit in an 8-bit pool: code_steps [N,n_tok,Hv,dk,dv] and scale_steps
+    [N,n_tok,Hv,dk] of gdn2_decode_multi_q8 into codes and scales. Returns (codes, scales)."""
+    _, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
+    dev = codes.device
+    N, n_tok = code_steps.shape[:2] if isinstance(code_steps, torch.Tensor) and code_steps.dim() == 5 else (0, 0)
+    _expect("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, dev)
+    _expect("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, dev)
+    _expect("index", index, (N,), torch.int32, dev)
+    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
+    with _at(dev, stream):
+        _check(load_library().gdn2_state_commit_q8(
+            N, h_v, dk, dv, n_tok, code_steps.data_ptr(), scale_steps.data_ptr(), index.data_ptr(), _p(slots),
+            codes.data_ptr(), scales.data_ptr(), n_slots, _raw_stream(dev, stream)))
+    return codes, scales
 
 
 def gdn2_device_status(stream=None) -> int:

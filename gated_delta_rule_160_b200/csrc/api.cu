@@ -32,8 +32,6 @@ gdn2_status ok() {
     return GDN2_OK;
 }
 
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
 // A pointer the GPU can dereference as device memory (plain or managed allocations).
 bool is_device_ptr(const void* ptr) {
     cudaPointerAttributes attr;
@@ -70,6 +68,7 @@ struct NamedPtr {
     const char* name;
     const void* ptr;
     bool required;
+    unsigned align = 16;
 };
 
 gdn2_status check_ptrs(const NamedPtr* ps, int n) {
@@ -78,8 +77,8 @@ gdn2_status check_ptrs(const NamedPtr* ps, int n) {
             if (ps[i].required) return fail(GDN2_ERR_INVALID_ARG, "%s is NULL", ps[i].name);
             continue;
         }
-        if (!aligned16(ps[i].ptr))
-            return fail(GDN2_ERR_INVALID_ARG, "%s = %p is not 16-byte aligned", ps[i].name, ps[i].ptr);
+        if (reinterpret_cast<uintptr_t>(ps[i].ptr) & (ps[i].align - 1u))
+            return fail(GDN2_ERR_INVALID_ARG, "%s = %p is not %u-byte aligned", ps[i].name, ps[i].ptr, ps[i].align);
         if (!is_device_ptr(ps[i].ptr))
             return fail(GDN2_ERR_INVALID_ARG, "%s = %p is not device memory", ps[i].name, ps[i].ptr);
     }
@@ -240,9 +239,8 @@ gdn2_status gdn2_decode_step(const gdn2_shape* shape, const void* q, const void*
 
 namespace {
 
-gdn2_status decode_multi(bool prologue, const gdn2_shape* shape, int n_tok, const int32_t* slots, const void* q,
-                         const void* k, const void* v, const void* la, const void* b, const void* w, float* S_pool,
-                         int n_slots, void* o, float* S_steps, gdn2_stream_t stream) {
+// What the serving decodes ask of their shape, token count and pool.
+gdn2_status check_serving(const gdn2_shape* shape, int n_tok, const int32_t* slots, int n_slots) {
     gdn2_status st = check_shape(shape);
     if (st != GDN2_OK) return st;
     if (n_tok < 1 || n_tok > GDN2_DECODE_MAX_TOKENS)
@@ -253,6 +251,14 @@ gdn2_status decode_multi(bool prologue, const gdn2_shape* shape, int n_tok, cons
     if (n_slots < 1 || (!slots && n_slots < shape->n_seq))
         return fail(GDN2_ERR_INVALID_ARG, "n_slots = %d too small (n_seq = %d, slots %s)", n_slots, shape->n_seq,
                     slots ? "given" : "NULL");
+    return GDN2_OK;
+}
+
+gdn2_status decode_multi(bool prologue, const gdn2_shape* shape, int n_tok, const int32_t* slots, const void* q,
+                         const void* k, const void* v, const void* la, const void* b, const void* w, float* S_pool,
+                         int n_slots, void* o, float* S_steps, gdn2_stream_t stream) {
+    gdn2_status st = check_serving(shape, n_tok, slots, n_slots);
+    if (st != GDN2_OK) return st;
     if ((long long)shape->n_seq * shape->h_v > 0x7fffffffLL || (long long)n_slots * shape->h_v > 0x7fffffffLL)
         return fail(GDN2_ERR_UNSUPPORTED, "n_seq * h_v or n_slots * h_v too large for one launch");
     if ((long long)n_slots * shape->h_v * shape->dk > 0x7fffffffLL)  // state rows, addressed by TMA
@@ -335,6 +341,156 @@ gdn2_status gdn2_chunk_bwd(const gdn2_shape* shape, const void* q, const void* k
     cudaError_t e = launch_bwd(p, shape->dtype, dO, dS_T, dq, dk, dv, dlog_alpha, db, dw, dS0, workspace,
                                reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "backward kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- around the state pool
+namespace {
+
+gdn2_status check_states(int n_seq, int h_v, int dk, int dv, const int32_t* slots, int n_slots) {
+    const gdn2_shape sh{n_seq, 0, 1, h_v, dk, dv, GDN2_F32, GDN2_F32};
+    gdn2_status st = check_shape(&sh);
+    if (st != GDN2_OK) return st;
+    if (n_slots < 1 || (!slots && n_slots < n_seq))
+        return fail(GDN2_ERR_INVALID_ARG, "n_slots = %d too small (n_seq = %d, slots %s)", n_slots, n_seq,
+                    slots ? "given" : "NULL");
+    return GDN2_OK;
+}
+
+gdn2_status check_format(gdn2_q8_format fmt) {
+    if (fmt != GDN2_Q8_INT8 && fmt != GDN2_Q8_E4M3) return fail(GDN2_ERR_INVALID_ARG, "unknown 8-bit format %d", (int)fmt);
+    return GDN2_OK;
+}
+
+gdn2_status state_cache(bool store, int n_seq, int h_v, int dk, int dv, gdn2_q8_format fmt, float* S, const int32_t* slots,
+                        void* codes, float* scales, int n_slots, gdn2_stream_t stream) {
+    gdn2_status st = check_states(n_seq, h_v, dk, dv, slots, n_slots);
+    if (st == GDN2_OK) st = check_format(fmt);
+    if (st != GDN2_OK) return st;
+    const NamedPtr ps[] = {{"S", S, true}, {"codes", codes, true}, {"scales", scales, true}, {"slots", slots, false, 4}};
+    st = check_ptrs(ps, (int)(sizeof ps / sizeof ps[0]));
+    if (st != GDN2_OK) return st;
+    const StateCacheArgs a{n_seq, h_v, dk, dv, n_slots, S, slots, codes, scales};
+    cudaError_t e = launch_state_cache(store, a, fmt, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "state %s kernel launch: %s", store ? "store" : "load", cudaGetErrorString(e));
+    return ok();
+}
+
+gdn2_status state_commit(bool q8, int n_seq, int h_v, int dk, int dv, int n_tok, const void* steps, const float* step_scales,
+                         const int32_t* index, const int32_t* slots, void* pool, float* scales, int n_slots,
+                         gdn2_stream_t stream) {
+    gdn2_status st = check_states(n_seq, h_v, dk, dv, slots, n_slots);
+    if (st != GDN2_OK) return st;
+    if (n_tok < 1 || n_tok > GDN2_DECODE_MAX_TOKENS)
+        return fail(GDN2_ERR_INVALID_ARG, "n_tok = %d outside 1..%d", n_tok, GDN2_DECODE_MAX_TOKENS);
+    const NamedPtr ps[] = {{q8 ? "code_steps" : "S_steps", steps, true}, {"scale_steps", step_scales, q8}, {"index", index, true, 4},
+                           {"slots", slots, false, 4}, {q8 ? "codes" : "S_pool", pool, true}, {"scales", scales, q8}};
+    st = check_ptrs(ps, (int)(sizeof ps / sizeof ps[0]));
+    if (st != GDN2_OK) return st;
+    const size_t elts = (size_t)h_v * dk * dv, rows = (size_t)h_v * dk;
+    cudaError_t e = launch_state_commit(steps, step_scales, index, slots, pool, scales, n_seq, n_tok, n_slots, q8 ? elts : 4 * elts,
+                                        q8 ? 4 * rows : 0, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "state commit kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+gdn2_status decode_multi_q8(bool prologue, const gdn2_shape* shape, gdn2_q8_format fmt, int n_tok, const int32_t* slots,
+                            const int32_t* slots_out, const void* q, const void* k, const void* v, const void* la,
+                            const void* b, const void* w, void* codes, float* scales, int n_slots, void* o,
+                            void* code_steps, float* scale_steps, gdn2_stream_t stream) {
+    gdn2_status st = check_serving(shape, n_tok, slots, n_slots);
+    if (st == GDN2_OK) st = check_format(fmt);
+    if (st != GDN2_OK) return st;
+    if ((code_steps == nullptr) != (scale_steps == nullptr))
+        return fail(GDN2_ERR_INVALID_ARG, "code_steps and scale_steps are given together or not at all");
+    const NamedPtr ps[] = {
+        {"q", q, true}, {"k", k, true}, {"v", v, true}, {prologue ? "a" : "log_alpha", la, true}, {"b", b, true},
+        {"w", w, true}, {"codes", codes, true}, {"scales", scales, true}, {"o", o, true}, {"slots", slots, false, 4},
+        {"slots_out", slots_out, false, 4}, {"code_steps", code_steps, false}, {"scale_steps", scale_steps, false},
+    };
+    st = check_ptrs(ps, (int)(sizeof ps / sizeof ps[0]));
+    if (st != GDN2_OK) return st;
+    Params p = make_params(shape, q, k, v, prologue ? nullptr : static_cast<const float*>(la), b, w, nullptr, nullptr, o,
+                           nullptr);
+    p.prologue = prologue;
+    p.a_raw = prologue ? la : nullptr;
+    p.n_tok = n_tok;
+    p.slots = slots;
+    p.n_slots = n_slots;
+    const Q8Args a{fmt, shape->dtype == GDN2_BF16, shape->o_dtype == GDN2_BF16, slots_out, codes, scales, code_steps, scale_steps};
+    cudaError_t e = launch_decode_q8(p, a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "8-bit decode kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn2_status gdn2_state_store(int n_seq, int h_v, int dk, int dv, gdn2_q8_format format, const float* S, const int32_t* slots,
+                             void* codes, float* scales, int n_slots, gdn2_stream_t stream) {
+    return state_cache(true, n_seq, h_v, dk, dv, format, const_cast<float*>(S), slots, codes, scales, n_slots, stream);
+}
+
+gdn2_status gdn2_state_load(int n_seq, int h_v, int dk, int dv, gdn2_q8_format format, const void* codes, const float* scales,
+                            int n_slots, const int32_t* slots, float* S, gdn2_stream_t stream) {
+    return state_cache(false, n_seq, h_v, dk, dv, format, S, slots, const_cast<void*>(codes), const_cast<float*>(scales), n_slots,
+                       stream);
+}
+
+gdn2_status gdn2_decode_multi_q8(const gdn2_shape* shape, gdn2_q8_format format, int n_tok, const int32_t* slots,
+                                 const int32_t* slots_out, const void* q, const void* k, const void* v, const float* log_alpha,
+                                 const void* b, const void* w, void* codes, float* scales, int n_slots, void* o,
+                                 void* code_steps, float* scale_steps, gdn2_stream_t stream) {
+    return decode_multi_q8(false, shape, format, n_tok, slots, slots_out, q, k, v, log_alpha, b, w, codes, scales, n_slots, o,
+                           code_steps, scale_steps, stream);
+}
+
+gdn2_status gdn2_decode_multi_q8_prologue(const gdn2_shape* shape, gdn2_q8_format format, int n_tok, const int32_t* slots,
+                                          const int32_t* slots_out, const void* q_raw, const void* k_raw, const void* v,
+                                          const void* a_raw, const void* b_raw, const void* w_raw, void* codes, float* scales,
+                                          int n_slots, void* o, void* code_steps, float* scale_steps, gdn2_stream_t stream) {
+    return decode_multi_q8(true, shape, format, n_tok, slots, slots_out, q_raw, k_raw, v, a_raw, b_raw, w_raw, codes, scales,
+                           n_slots, o, code_steps, scale_steps, stream);
+}
+
+gdn2_status gdn2_state_commit(int n_seq, int h_v, int dk, int dv, int n_tok, const float* S_steps, const int32_t* index,
+                              const int32_t* slots, float* S_pool, int n_slots, gdn2_stream_t stream) {
+    return state_commit(false, n_seq, h_v, dk, dv, n_tok, S_steps, nullptr, index, slots, S_pool, nullptr, n_slots, stream);
+}
+
+gdn2_status gdn2_state_commit_q8(int n_seq, int h_v, int dk, int dv, int n_tok, const void* code_steps, const float* scale_steps,
+                                 const int32_t* index, const int32_t* slots, void* codes, float* scales, int n_slots,
+                                 gdn2_stream_t stream) {
+    return state_commit(true, n_seq, h_v, dk, dv, n_tok, code_steps, scale_steps, index, slots, codes, scales, n_slots, stream);
+}
+
+gdn2_status gdn2_verify_drafts(int n_seq, int n_draft, int vocab, gdn2_dtype dtype, const void* target_probs, const void* draft_probs,
+                               const int32_t* draft_tokens, const int32_t* n_drafted, const float* u_accept,
+                               const float* u_sample, int32_t* n_accepted, int32_t* tokens, gdn2_stream_t stream) {
+    if (n_seq < 1 || n_seq > 65535) return fail(GDN2_ERR_INVALID_ARG, "n_seq = %d outside [1, 65535]", n_seq);
+    if (n_draft < 0) return fail(GDN2_ERR_INVALID_ARG, "n_draft = %d is negative", n_draft);
+    if (n_draft > GDN2_VERIFY_MAX_DRAFTS)
+        return fail(GDN2_ERR_UNSUPPORTED, "n_draft = %d above %d", n_draft, GDN2_VERIFY_MAX_DRAFTS);
+    if (vocab < 1) return fail(GDN2_ERR_INVALID_ARG, "vocab = %d must be positive", vocab);
+    if (vocab > GDN2_VERIFY_MAX_VOCAB) return fail(GDN2_ERR_UNSUPPORTED, "vocab = %d above %d", vocab, GDN2_VERIFY_MAX_VOCAB);
+    if (dtype != GDN2_F32 && dtype != GDN2_BF16) return fail(GDN2_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    const bool drafts = n_draft > 0;
+    const unsigned es = dtype == GDN2_F32 ? 4 : 2;
+    const NamedPtr ps[] = {
+        {"target_probs", target_probs, true, es}, {"draft_probs", drafts ? draft_probs : nullptr, false, es},
+        {"draft_tokens", drafts ? draft_tokens : nullptr, drafts, 4}, {"n_drafted", n_drafted, false, 4},
+        {"u_accept", drafts ? u_accept : nullptr, drafts, 4}, {"u_sample", u_sample, true, 4},
+        {"n_accepted", n_accepted, true, 4}, {"tokens", tokens, true, 4},
+    };
+    gdn2_status st = check_ptrs(ps, (int)(sizeof ps / sizeof ps[0]));
+    if (st != GDN2_OK) return st;
+    const VerifyArgs a{n_seq, n_draft, vocab, target_probs, drafts ? draft_probs : nullptr, draft_tokens, n_drafted, u_accept,
+                       u_sample, n_accepted, tokens};
+    cudaError_t e = launch_verify(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "verification kernel launch: %s", cudaGetErrorString(e));
     return ok();
 }
 

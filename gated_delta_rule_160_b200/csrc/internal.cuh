@@ -139,6 +139,37 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(x);
 }
 
+// The 8-bit pool of a decode (gdn2_decode_multi_q8); everything else about the call is in Params.
+struct Q8Args {
+    gdn2_q8_format fmt;
+    int bf16, o_bf16;          // element types of the tokens and of o
+    const int32_t* slots_out;  // nullable: slot that each state is written to
+    void* codes;
+    float* scales;
+    void* code_steps;          // nullable: the state after each token
+    float* scale_steps;
+};
+
+struct StateCacheArgs {
+    int n_seq, h_v, dk, dv, n_slots;
+    float* S;                  // read by a store, written by a load
+    const int32_t* slots;      // nullable
+    void* codes;
+    float* scales;
+};
+
+struct VerifyArgs {
+    int n_seq, n_draft, vocab;
+    const void* p;             // [n_seq, n_draft + 1, vocab]
+    const void* q;             // [n_seq, n_draft, vocab], nullable
+    const int32_t* drafts;
+    const int32_t* n_drafted;  // nullable
+    const float* u_accept;
+    const float* u_sample;
+    int32_t* n_accepted;
+    int32_t* tokens;
+};
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_recurrent(const Params& p, gdn2_dtype dt, gdn2_dtype odt, cudaStream_t s);
 cudaError_t launch_decode(const Params& p, gdn2_dtype dt, gdn2_dtype odt, cudaStream_t s);
@@ -159,6 +190,12 @@ cudaError_t launch_check_seqlens(const Params& p, cudaStream_t s);
 size_t bwd_workspace_bytes(const gdn2_shape* sh);
 cudaError_t launch_bwd(const Params& p, gdn2_dtype dt, const float* dO, const float* dS_T, float* dq, float* dk,
                        float* dv, float* dla, float* db, float* dw, float* dS0, void* workspace, cudaStream_t s);
+// The serving operators around the state pool.
+cudaError_t launch_decode_q8(const Params& p, const Q8Args& a, cudaStream_t s);
+cudaError_t launch_state_cache(bool store, const StateCacheArgs& a, gdn2_q8_format fmt, cudaStream_t s);
+cudaError_t launch_state_commit(const void* steps, const float* step_scales, const int32_t* index, const int32_t* slots, void* pool,
+                                float* scales, int n_seq, int n_tok, int n_slots, size_t bytes, size_t scale_bytes, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, gdn2_dtype dt, cudaStream_t s);
 // Record a failure in the calling thread's error string and return st.
 gdn2_status report_error(gdn2_status st, const char* msg);
 

@@ -1,0 +1,83 @@
+// q8.cuh -- the 8-bit state format: codes (int8 or e4m3) and one fp32 scale per key row.
+//
+// A state S [dk, dv] is kept as codes [dk, dv] and scales [dk]. With a = max_j |S_ij| over a
+// key row i and M = 127 (int8) or 448 (e4m3, its largest finite value):
+//   a infinite or NaN   scale = NaN, codes 0      the row reads back as NaN: a state that has
+//                                                 blown up stays visible
+//   a < 2^-100          scale = 0,   codes 0      (2^-100: 1 / a and a / M stay normal numbers)
+//   otherwise           scale = fl(a / M), code_ij = RN(fl(S_ij fl(M / a)))
+// and read back as S_ij = fl(code_ij scale). Every fl() is fp32 rounding to nearest. The two
+// roundings before the code's own move it across a border between codes for about one value in
+// 10^5, by 2^-23 of the row's largest magnitude; the code's own rounding is off by up to half a
+// step: a / 254 (int8), or 2^-4 of the value and a / 458752 near zero (e4m3). One scale per
+// key row because the decay acts on key rows: rows of one state differ in magnitude by their
+// decays, a row's own values do not.
+#pragma once
+
+#include "internal.cuh"
+
+namespace gdn2 {
+
+constexpr float kQ8Tiny = 7.888609052210118e-31f;  // 2^-100
+
+template <int kFmt> struct Q8;
+template <> struct Q8<GDN2_Q8_INT8> { static constexpr float kTop = 127.f; };
+template <> struct Q8<GDN2_Q8_E4M3> { static constexpr float kTop = 448.f; };
+
+// Scale and inverse of a row from the bits of its largest magnitude; inv = 0 marks a row whose
+// codes are 0.
+template <int kFmt>
+__device__ __forceinline__ void q8_scale(float amax, float& scale, float& inv) {
+    const bool finite = __float_as_uint(amax) < 0x7f800000u;
+    const bool keep = finite && amax >= kQ8Tiny;
+    scale = keep ? __fdiv_rn(amax, Q8<kFmt>::kTop) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
+    inv = keep ? __fdiv_rn(Q8<kFmt>::kTop, amax) : 0.f;
+}
+
+// Magnitudes are compared as integers: ordered like the values, and an infinity or a NaN wins.
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Four codes of x * inv, packed in column order.
+template <int kFmt>
+__device__ __forceinline__ uint32_t q8_pack(float4 x, float inv) {
+    x.x = __fmul_rn(x.x, inv); x.y = __fmul_rn(x.y, inv); x.z = __fmul_rn(x.z, inv); x.w = __fmul_rn(x.w, inv);
+    uint32_t r;
+    if (kFmt == GDN2_Q8_INT8) {
+        // |x| <= 127.00002: adding 1.5 2^23 rounds to the nearest whole number, ties to even, and
+        // leaves it as the low byte
+        const float c = 12582912.f;
+        const uint32_t a = __float_as_uint(__fadd_rn(x.x, c)), b = __float_as_uint(__fadd_rn(x.y, c));
+        const uint32_t d = __float_as_uint(__fadd_rn(x.z, c)), e = __float_as_uint(__fadd_rn(x.w, c));
+        r = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
+    } else {
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y), "f"(x.x));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x.w), "f"(x.z));
+        r = (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+    return inv == 0.f ? 0u : r;
+}
+
+// The values of four codes, before the scale.
+template <int kFmt>
+__device__ __forceinline__ float4 q8_unpack(uint32_t c) {
+    if (kFmt == GDN2_Q8_INT8) {
+        // code + 128 as the low byte of 2^23's mantissa, then 2^23 + 128 taken off: exact
+        const uint32_t u = c ^ 0x80808080u;
+        const float m = 8388736.f;
+        return make_float4(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650)) - m,
+                           __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7651)) - m,
+                           __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7652)) - m,
+                           __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7653)) - m);
+    } else {
+        uint32_t lo, hi;  // e4m3 is exact in fp16, and fp16 in fp32
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(c & 0xffffu)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(c >> 16)));
+        float4 x;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(x.x), "=f"(x.y) : "r"(lo));
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(x.z), "=f"(x.w) : "r"(hi));
+        return x;
+    }
+}
+
+}  // namespace gdn2

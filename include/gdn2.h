@@ -235,6 +235,114 @@ GDN2_API gdn2_status gdn2_chunk_fwd_noalloc(const gdn2_shape* shape,
                                     void* o, float* S_T, gdn2_stream_t stream);
 
 /*
+ * 8-bit state cache. A pool of states at about a quarter of the fp32 bytes: codes
+ * [n_slots, h_v, dk, dv] (int8, or e4m3 bytes) and scales [n_slots, h_v, dk] float32, one per
+ * key row. With a = max_j |S_ij| over key row i and M = 127 (int8) or 448 (e4m3):
+ *   a infinite or NaN: scale NaN, codes 0 (the row reads back as NaN)
+ *   a < 2^-100:        scale 0, codes 0
+ *   otherwise:         scale = fl(a / M), code_ij = RN(fl(S_ij fl(M / a)))
+ * and S_ij reads back as fl(code_ij scale), fl being fp32 rounding. int8 codes are off by at most
+ * half a step, a / 254; e4m3 codes by 2^-4 of the value (a / 458752 near zero). int8 is the more
+ * exact one for rows whose values are of one magnitude, e4m3 keeps a row's small values in
+ * proportion. The pages describe fp32 states only; the format is an interface choice.
+ */
+typedef enum { GDN2_Q8_INT8 = 0, GDN2_Q8_E4M3 = 1 } gdn2_q8_format;
+
+/*
+ * Quantise n_seq states S [n_seq, h_v, dk, dv] float32 into their slots of the pool (slots: device
+ * int32 [n_seq]; NULL means slot n, and then n_slots must be at least n_seq). A sequence whose
+ * slot is negative or >= n_slots is skipped. Two active sequences must not share a slot, and S must
+ * not overlap the pool.
+ */
+GDN2_API gdn2_status gdn2_state_store(int n_seq, int h_v, int dk, int dv, gdn2_q8_format format,
+                             const float* S, const int32_t* slots,
+                             void* codes, float* scales, int n_slots, gdn2_stream_t stream);
+
+/*
+ * Read n_seq states back from their slots into S [n_seq, h_v, dk, dv] float32, for example as the
+ * S0 of a prefill. Sequences may share a slot. A sequence whose slot is negative or >= n_slots has
+ * nothing cached and gets the zero state.
+ */
+GDN2_API gdn2_status gdn2_state_load(int n_seq, int h_v, int dk, int dv, gdn2_q8_format format,
+                            const void* codes, const float* scales, int n_slots, const int32_t* slots,
+                            float* S, gdn2_stream_t stream);
+
+/*
+ * gdn2_decode_multi on an 8-bit pool: each state is read as codes, advanced through the n_tok
+ * tokens in fp32 and quantised as it is written.
+ *   slots_out (nullable: device int32 [n_seq]; NULL means the slots read) is where sequence n's
+ *   state is written, so that a sequence can go on from a shared prefix's slot without changing
+ *   it; with a negative or out-of-range value the state is written nowhere (o still is).
+ *   Several sequences may read one slot as long as none of the call writes it; a slot that one
+ *   sequence writes must not be read or written by another (they would race).
+ *   code_steps [n_seq, n_tok, h_v, dk, dv] and scale_steps [n_seq, n_tok, h_v, dk] (both or
+ *   neither; nullable) receive the state after each token, quantised; the state that the next
+ *   token goes on from is the unrounded one.
+ * Otherwise as gdn2_decode_multi (tokens, skipped sequences, n_tok); no TMA addresses the pool, so
+ * the limit on n_slots * h_v * dk does not apply.
+ */
+GDN2_API gdn2_status gdn2_decode_multi_q8(const gdn2_shape* shape, gdn2_q8_format format, int n_tok,
+                                 const int32_t* slots, const int32_t* slots_out,
+                                 const void* q, const void* k, const void* v,
+                                 const float* log_alpha, const void* b, const void* w,
+                                 void* codes, float* scales, int n_slots, void* o,
+                                 void* code_steps, float* scale_steps, gdn2_stream_t stream);
+
+/* gdn2_decode_multi_q8 with the pre-processing of gdn2_chunk_fwd_prologue fused in. */
+GDN2_API gdn2_status gdn2_decode_multi_q8_prologue(const gdn2_shape* shape, gdn2_q8_format format, int n_tok,
+                                          const int32_t* slots, const int32_t* slots_out,
+                                          const void* q_raw, const void* k_raw, const void* v,
+                                          const void* a_raw, const void* b_raw, const void* w_raw,
+                                          void* codes, float* scales, int n_slots, void* o,
+                                          void* code_steps, float* scale_steps, gdn2_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random numbers
+ * (speculative sampling; the pages have no counterpart, this completes the multi-token decode).
+ *   target_probs [n_seq, n_draft + 1, vocab] dtype: p_i, the target's distribution of the token
+ *     at place i (after the i drafted tokens before it); draft_probs [n_seq, n_draft, vocab]
+ *     dtype: q_i, what drafted token i was drawn from (NULL: each draft was certain, q_i is 1 at
+ *     the drafted token); draft_tokens int32 [n_seq, n_draft]
+ *   n_drafted (nullable: device int32 [n_seq]; NULL means n_draft) the sequence's drafted tokens,
+ *     m = min(n_drafted[n], n_draft); negative marks an inactive sequence
+ *   u_accept float32 [n_seq, n_draft], u_sample float32 [n_seq]: uniform random numbers in [0, 1)
+ * Token i < m is accepted while u_i q_i(t_i) < p_i(t_i). The first that is not, at place a, is
+ * replaced by a token of max(p_a - q_a, 0), or of p_a where that is zero everywhere; with a = m
+ * accepted, one more token comes from p_m. A token is drawn from weights r (they need not sum to
+ * 1) as the lowest j with r_0 + .. + r_j > u_sample (r_0 + .. + r_{vocab-1}), all in fp64.
+ *   n_accepted int32 [n_seq]: a (-1: inactive)
+ *   tokens int32 [n_seq, n_draft + 1]: the accepted tokens, the drawn one at place a, -1 behind
+ *     it (all -1: inactive). The drawn token is -1 where p_a has no weight at all.
+ * A probability that is negative, infinite or NaN counts as 0; a drafted token outside the vocabulary is
+ * never accepted; a random number outside [0, 1] counts as the nearest bound, NaN as a refusal or 0.
+ * Supported: n_draft 0..GDN2_VERIFY_MAX_DRAFTS, vocab 1..GDN2_VERIFY_MAX_VOCAB; any alignment of
+ * the rows (pointers aligned to their elements).
+ */
+#define GDN2_VERIFY_MAX_DRAFTS 31
+#define GDN2_VERIFY_MAX_VOCAB 4194304
+GDN2_API gdn2_status gdn2_verify_drafts(int n_seq, int n_draft, int vocab, gdn2_dtype dtype,
+                               const void* target_probs, const void* draft_probs,
+                               const int32_t* draft_tokens, const int32_t* n_drafted,
+                               const float* u_accept, const float* u_sample,
+                               int32_t* n_accepted, int32_t* tokens, gdn2_stream_t stream);
+
+/*
+ * Put back the state after the last accepted token: slot slots[n] of the pool (slots as for
+ * gdn2_decode_multi) becomes S_steps[n, index[n]], with S_steps [n_seq, n_tok, h_v, dk, dv] as
+ * gdn2_decode_multi wrote it and index device int32 [n_seq]. After a step over the last accepted
+ * token and the drafted ones, index is gdn2_verify_drafts's n_accepted. A sequence whose index is
+ * outside 0..n_tok-1, or whose slot is out of range, is left as it is. Two active sequences must
+ * not share a slot. gdn2_state_commit_q8 does the same in an 8-bit pool (either format).
+ */
+GDN2_API gdn2_status gdn2_state_commit(int n_seq, int h_v, int dk, int dv, int n_tok,
+                              const float* S_steps, const int32_t* index, const int32_t* slots,
+                              float* S_pool, int n_slots, gdn2_stream_t stream);
+GDN2_API gdn2_status gdn2_state_commit_q8(int n_seq, int h_v, int dk, int dv, int n_tok,
+                                 const void* code_steps, const float* scale_steps,
+                                 const int32_t* index, const int32_t* slots,
+                                 void* codes, float* scales, int n_slots, gdn2_stream_t stream);
+
+/*
  * Device-side status. The pages describe no interface, so this is an interface choice: some
  * errors can only be seen once the kernels run, after the call that queued them has
  * returned GDN2_OK. The kernels record them in a status word per device (bits below), and
