@@ -10,30 +10,64 @@
 // sum's rounding, ~1e-16, all but never crosses a border of the CDF, so the order of the sums does not show
 // in the tokens.
 //
-// The work is one row of p and one of q a sequence.
+// The work is one row of p and one of q a sequence, so a cluster of up to 8 CTAs shares a sequence: each warp
+// sums segments of 1024 weights (all 16-byte loads of a segment in flight at once), the CTAs exchange
+// their sums through distributed shared memory, and the CTA that holds the border scans its
+// segment sums and then that one segment again, out of L2. No workspace, no atomics on memory, one launch.
+#include <cooperative_groups.h>
+
 #include "internal.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace gdn2 {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kSeg = 1024;                                 // values per segment of the CDF
-constexpr int kMaxSeg = GDN2_VERIFY_MAX_VOCAB / kSeg;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSeg = 1024;         // values per segment of the CDF; a warp sums one at a time
+constexpr int kMaxCluster = 8;     // CTAs per sequence (the portable cluster size)
+constexpr int kMaxSeg = GDN2_VERIFY_MAX_VOCAB / kSeg / kMaxCluster;  // segments per CTA
 
 enum Mode { kPlain, kResidual, kOneHot };
 
-__device__ __forceinline__ double clean(float x) { return x > 0.f && x <= 3.402823466e38f ? (double)x : 0.0; }
+// A probability as it counts: positive and finite, else 0 (as integers, everything else is larger).
+__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) < 0x7f800000u ? x : 0.f; }
 
-// The weight of token j in the row that the token is drawn from.
+// 16 bytes of probabilities as floats.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ void get(uint4 v, float* x) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ void get(uint4 v, float* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+// The weight of a token in the row that the next token is drawn from.
+__device__ __forceinline__ double weight(float p, float q, bool masked) {
+    p = clean(p);
+    q = clean(q);
+    return p > q && !masked ? (double)p - (double)q : 0.0;
+}
+
 template <typename T>
 struct Row {
     const T* p;
-    const T* q;
-    int t, mode;
+    const T* q;  // kResidual
+    int t;       // kOneHot: the token left out
+    int mode;
     __device__ __forceinline__ double at(int j) const {
-        const double x = clean(to_f32(p[j]));
-        if (mode == kResidual) return fmax(x - clean(to_f32(q[j])), 0.0);
-        return mode == kOneHot && j == t ? 0.0 : x;
+        return weight(to_f32(p[j]), mode == kResidual ? to_f32(q[j]) : 0.f, mode == kOneHot && j == t);
     }
 };
 
@@ -51,19 +85,61 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
     return x;
 }
 
-template <typename T>
+// This lane's share of one segment's sum. All loads of a segment are issued before the first use.
+template <typename T, bool kVec>
+__device__ __forceinline__ double segment(const Row<T>& row, int j0, int V, int lane) {
+    double x = 0.0;
+    if (kVec) {  // rows start at 16-byte boundaries and hold whole vectors
+        constexpr int N = Vec<T>::kN, IT = kSeg / (32 * N);
+        uint4 pv[IT], qv[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int j = j0 + (i * 32 + lane) * N;
+            pv[i] = j < V ? __ldg(reinterpret_cast<const uint4*>(row.p + j)) : make_uint4(0, 0, 0, 0);
+            qv[i] = j < V && row.mode == kResidual ? __ldg(reinterpret_cast<const uint4*>(row.q + j)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int j = j0 + (i * 32 + lane) * N;
+            float pf[N], qf[N];
+            Vec<T>::get(pv[i], pf);
+            Vec<T>::get(qv[i], qf);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x += weight(pf[e], qf[e], row.mode == kOneHot && j + e == row.t);
+        }
+    } else {
+        constexpr int U = 16;
+        for (int i0 = 0; i0 < kSeg / 32; i0 += U) {
+            float pf[U], qf[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int j = j0 + (i0 + i) * 32 + lane;
+                pf[i] = j < V ? to_f32(row.p[j]) : 0.f;
+                qf[i] = j < V && row.mode == kResidual ? to_f32(row.q[j]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) x += weight(pf[i], qf[i], row.mode == kOneHot && j0 + (i0 + i) * 32 + lane == row.t);
+        }
+    }
+    return x;
+}
+
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ double seg_sum[kMaxSeg];
     __shared__ double wsum[kWarps];
-    __shared__ int s_taken, s_mode, s_found, s_last;
-    __shared__ double s_total;
-    const int n = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    __shared__ double cta_total[2];  // this CTA's part of the row, read by the whole cluster
+    __shared__ double s_before;
+    __shared__ int s_taken, s_seg, s_found, s_last;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int n = blockIdx.x / ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int V = a.vocab, k = a.n_draft;
     int m = a.n_drafted ? a.n_drafted[n] : k;
     int* tokens = a.tokens + (size_t)n * (k + 1);
     if (m < 0) {  // an inactive sequence
-        for (int i = tid; i <= k; i += kThreads) tokens[i] = -1;
-        if (tid == 0) a.n_accepted[n] = -1;
+        if (rank == 0 && tid <= k) tokens[tid] = -1;
+        if (rank == 0 && tid == 0) a.n_accepted[n] = -1;
         return;
     }
     m = min(m, k);
@@ -75,8 +151,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         if (lane < m) {
             const int t = drafts[lane];
             if (t >= 0 && t < V) {
-                const double pt = clean(to_f32(P[(size_t)lane * V + t])), qt = Q ? clean(to_f32(Q[(size_t)lane * V + t])) : 1.0;
-                yes = (double)a.u_accept[(size_t)n * k + lane] * qt < pt;
+                const float pt = clean(to_f32(P[(size_t)lane * V + t])), qt = Q ? clean(to_f32(Q[(size_t)lane * V + t])) : 1.f;
+                yes = (double)a.u_accept[(size_t)n * k + lane] * (double)qt < (double)pt;
             }
         }
         const unsigned no = ~__ballot_sync(0xffffffffu, yes);  // lane m's bit is set: m <= 31
@@ -87,101 +163,143 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     const bool refused = taken < m;
     Row<T> row{P + (size_t)taken * V, refused && Q ? Q + (size_t)taken * V : nullptr, refused ? drafts[taken] : -1,
                !refused ? kPlain : (Q ? kResidual : kOneHot)};
-    const int segs = (V + kSeg - 1) / kSeg;
-    double total;
-    for (;;) {
-        for (int s = warp; s < segs; s += kWarps) {
-            double x = 0.0;
-            const int end = min(V, (s + 1) * kSeg);
-            for (int j = s * kSeg + lane; j < end; j += 32) x += row.at(j);
-            x = warp_sum(x);
+
+    // this CTA's segments, and their sum
+    const int segs = (V + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
+    const int first = min(rank * per, segs), count = min(per, segs - first);
+    double part[kMaxCluster], total = 0.0;
+    for (int pass = 0;; ++pass) {
+        for (int s = warp; s < count; s += kWarps) {
+            const double x = warp_sum(segment<T, kVec>(row, (first + s) * kSeg, V, lane));
             if (lane == 0) seg_sum[s] = x;
         }
         __syncthreads();
         if (warp == 0) {
             double x = 0.0;
-            for (int s = lane; s < segs; s += 32) x += seg_sum[s];
+            for (int s = lane; s < count; s += 32) x += seg_sum[s];
             x = warp_sum(x);
-            if (lane == 0) s_total = x;
+            if (lane == 0) cta_total[pass] = x;
         }
-        __syncthreads();
-        total = s_total;
+        cluster.sync();
+        total = 0.0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            part[c] = c < ctas ? *cluster.map_shared_rank(&cta_total[pass], c) : 0.0;
+            total += part[c];
+        }
         if (total > 0.0 || row.mode == kPlain) break;
         row.mode = kPlain;  // nothing is left of the row: its own probabilities
     }
-    int token = -1;
-    if (total > 0.0) {
-        const double u = fmin(fmax((double)a.u_sample[n], 0.0), 1.0);
-        const double target = u * total;
-        // the segment that the border falls into: the first whose running sum passes the target, else the last
-        // that is not empty
-        if (warp == 0) {
-            double before = 0.0, at = 0.0;
-            int found = -1, last = -1;
-            double last_before = 0.0;
-            for (int s0 = 0; s0 < segs && found < 0; s0 += 32) {
-                const double x = s0 + lane < segs ? seg_sum[s0 + lane] : 0.0;
-                const double c = before + warp_scan(x, lane);
-                const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && c > target);
-                const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    found = s0 + l;
-                    at = __shfl_sync(0xffffffffu, c - x, l);
-                } else if (some) {
-                    const int l = 31 - __clz(some);
-                    last = s0 + l;
-                    last_before = __shfl_sync(0xffffffffu, c - x, l);
-                }
-                before = __shfl_sync(0xffffffffu, c, 31);
-            }
-            if (lane == 0) {
-                s_mode = found >= 0 ? found : last;
-                s_total = found >= 0 ? at : last_before;
-                s_found = 0x7fffffff;
-                s_last = -1;
-            }
-        }
-        __syncthreads();
-        // the token within the segment
-        const int j0 = s_mode * kSeg + tid * (kSeg / kThreads);
-        double x[kSeg / kThreads], mine = 0.0;
+    cluster.barrier_arrive();  // no more reads of other CTAs' shared memory
+    // Every CTA has the same sums, so all agree on the one that holds the border: the first whose
+    // running sum passes the target, else (a random number of 1, a rounding) the last with any weight.
+    const double target = fmin(fmax((double)a.u_sample[n], 0.0), 1.0) * total;
+    int owner = 0;
+    double run = 0.0, before = 0.0;
+    bool found_cta = false;
 #pragma unroll
-        for (int i = 0; i < kSeg / kThreads; ++i) {
-            x[i] = j0 + i < V ? row.at(j0 + i) : 0.0;
-            mine += x[i];
+    for (int c = 0; c < kMaxCluster; ++c) {
+        if (part[c] > 0.0 && !found_cta) {
+            owner = c;
+            before = run;
+            found_cta = run + part[c] > target;
         }
-        const double c = warp_scan(mine, lane);
-        if (lane == 31) wsum[warp] = c;
-        __syncthreads();
-        double run = s_total + c - mine;
-        for (int w = 0; w < warp; ++w) run += wsum[w];
-        int found = 0x7fffffff, last = -1;
-#pragma unroll
-        for (int i = 0; i < kSeg / kThreads; ++i) {
-            run += x[i];
-            if (x[i] > 0.0) {
-                if (run > target) found = min(found, j0 + i);
-                last = j0 + i;
-            }
-        }
-        if (found != 0x7fffffff) atomicMin(&s_found, found);
-        if (last >= 0) atomicMax(&s_last, last);
-        __syncthreads();
-        token = s_found != 0x7fffffff ? s_found : s_last;
+        run += part[c];
     }
-    for (int i = tid; i <= k; i += kThreads) tokens[i] = i < taken ? drafts[i] : (i == taken ? token : -1);
-    if (tid == 0) a.n_accepted[n] = taken;
+    if (rank == owner) {
+        int token = -1;
+        if (total > 0.0) {
+            // the segment, by the same rule
+            if (warp == 0) {
+                double run = before, at = 0.0, last_at = 0.0;
+                int found = -1, last = -1;
+                for (int s0 = 0; s0 < count && found < 0; s0 += 32) {
+                    const double x = s0 + lane < count ? seg_sum[s0 + lane] : 0.0;
+                    const double c = run + warp_scan(x, lane);
+                    const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
+                    const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && c > target);
+                    if (hit) {
+                        const int l = __ffs(hit) - 1;
+                        found = s0 + l;
+                        at = __shfl_sync(0xffffffffu, c - x, l);
+                    } else if (some) {
+                        const int l = 31 - __clz(some);
+                        last = s0 + l;
+                        last_at = __shfl_sync(0xffffffffu, c - x, l);
+                    }
+                    run = __shfl_sync(0xffffffffu, c, 31);
+                }
+                if (lane == 0) {
+                    s_seg = found >= 0 ? found : last;
+                    s_before = found >= 0 ? at : last_at;
+                    s_found = 0x7fffffff;
+                    s_last = -1;
+                }
+            }
+            __syncthreads();
+            // the token within the segment
+            constexpr int E = kSeg / kThreads;
+            const int j0 = (first + s_seg) * kSeg + tid * E;
+            double x[E], sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                x[i] = j0 + i < V ? row.at(j0 + i) : 0.0;
+                sum += x[i];
+            }
+            const double c = warp_scan(sum, lane);
+            if (lane == 31) wsum[warp] = c;
+            __syncthreads();
+            double run = s_before + (c - sum);
+            for (int w = 0; w < warp; ++w) run += wsum[w];
+            int found = 0x7fffffff, last = -1;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                run += x[i];
+                if (x[i] > 0.0) {
+                    if (run > target) found = min(found, j0 + i);
+                    last = j0 + i;
+                }
+            }
+            if (found != 0x7fffffff) atomicMin(&s_found, found);
+            if (last >= 0) atomicMax(&s_last, last);
+            __syncthreads();
+            token = s_found != 0x7fffffff ? s_found : s_last;
+        }
+        if (tid <= k) tokens[tid] = tid < taken ? drafts[tid] : (tid == taken ? token : -1);
+        if (tid == 0) a.n_accepted[n] = taken;
+    }
+    cluster.barrier_wait();  // this CTA's sums stay readable until all have read them
+}
+
+template <typename T, bool kVec>
+cudaError_t launch(const VerifyArgs& a, cudaStream_t st) {
+    // one segment for each warp of the cluster, as far as 8 CTAs go
+    const int segs = (a.vocab + kSeg - 1) / kSeg;
+    int ctas = 1;
+    while (ctas < kMaxCluster && ctas * kWarps < segs) ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.n_seq * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const VerifyArgs& a, cudaStream_t st) {
+    const auto whole = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; };
+    return whole(a.p) && whole(a.q) && a.vocab % Vec<T>::kN == 0 ? launch<T, true>(a, st) : launch<T, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, gdn2_dtype dt, cudaStream_t st) {
-    if (dt == GDN2_F32)
-        verify_kernel<float><<<a.n_seq, kThreads, 0, st>>>(a);
-    else
-        verify_kernel<__nv_bfloat16><<<a.n_seq, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return dt == GDN2_F32 ? launch_t<float>(a, st) : launch_t<__nv_bfloat16>(a, st);
 }
 
 }  // namespace gdn2
