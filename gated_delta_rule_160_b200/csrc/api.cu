@@ -121,15 +121,16 @@ int gdn2_version(void) { return 200; }
 gdn2_status gdn2_device_status(unsigned int* flags, gdn2_stream_t stream) {
     if (!flags) return fail(GDN2_ERR_INVALID_ARG, "flags is NULL");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int w[4] = {0u, 0u, 0u, 0u};
+    unsigned int w[5] = {0u, 0u, 0u, 0u, 0u};
     cudaError_t e = cudaStreamSynchronize(s);  // the work queued so far has run
     if (e == cudaSuccess) e = read_clear_status_chunk_tc(&w[0], s);
     if (e == cudaSuccess) e = read_clear_status_recurrent(&w[1], s);
     if (e == cudaSuccess) e = read_clear_status_schedule(&w[2], s);
     if (e == cudaSuccess) e = read_clear_status_decode(&w[3], s);
+    if (e == cudaSuccess) e = read_clear_status_decode_q8(&w[4], s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);  // the reads have landed in w
     if (e != cudaSuccess) return fail(GDN2_ERR_CUDA, "device status: %s", cudaGetErrorString(e));
-    *flags = w[0] | w[1] | w[2] | w[3];
+    *flags = w[0] | w[1] | w[2] | w[3] | w[4];
     return ok();
 }
 

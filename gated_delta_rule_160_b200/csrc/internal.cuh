@@ -182,6 +182,7 @@ cudaError_t read_clear_status_chunk_tc(unsigned int* out, cudaStream_t s);
 cudaError_t read_clear_status_recurrent(unsigned int* out, cudaStream_t s);
 cudaError_t read_clear_status_schedule(unsigned int* out, cudaStream_t s);
 cudaError_t read_clear_status_decode(unsigned int* out, cudaStream_t s);
+cudaError_t read_clear_status_decode_q8(unsigned int* out, cudaStream_t s);
 // cuTensorMapEncodeTiled from the driver (as a void*; NULL if unavailable)
 void* tensor_map_encoder();
 // Validate cu_seqlens on the device (flags kStatusBadSeqlens); used where no order kernel runs.

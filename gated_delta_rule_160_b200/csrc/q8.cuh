@@ -80,4 +80,58 @@ __device__ __forceinline__ float4 q8_unpack(uint32_t c) {
     }
 }
 
+// The same for two rows at once, as pairs (row 0, row 1) per column; N columns in the low bytes of
+// each row's word.
+template <int kFmt, int N>
+__device__ __forceinline__ void q8_unpack_pair(uint32_t w0, uint32_t w1, float2* x) {
+    if (kFmt == GDN2_Q8_INT8) {
+        const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
+        const float2 m = make_float2(-8388736.f, -8388736.f);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            x[j] = fadd2(make_float2(__uint_as_float(__byte_perm(u0, 0x4b000000u, 0x7650 | j)),
+                                     __uint_as_float(__byte_perm(u1, 0x4b000000u, 0x7650 | j))), m);
+    } else {
+        const float4 a = q8_unpack<kFmt>(w0), b = q8_unpack<kFmt>(w1);
+        x[0] = make_float2(a.x, b.x);
+        x[1] = make_float2(a.y, b.y);
+        if (N == 4) {
+            x[2 % N] = make_float2(a.z, b.z);
+            x[3 % N] = make_float2(a.w, b.w);
+        }
+    }
+}
+
+// Codes of two rows' values, inv = (row 0's, row 1's), without q8_pack's rule for inv = 0.
+template <int kFmt, int N>
+__device__ __forceinline__ void q8_pack_pair(const float2* x, float2 inv, uint32_t& w0, uint32_t& w1) {
+    float2 y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = j < N ? fmul2(x[j % N], inv) : make_float2(0.f, 0.f);
+    if (kFmt == GDN2_Q8_INT8) {
+        const float2 c = make_float2(12582912.f, 12582912.f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = fadd2(y[j], c);
+        const auto pack = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040); };
+        w0 = pack(y[0].x, y[1].x);
+        w1 = pack(y[0].y, y[1].y);
+        if (N == 4) {
+            w0 = __byte_perm(w0, pack(y[2].x, y[3].x), 0x5410);
+            w1 = __byte_perm(w1, pack(y[2].y, y[3].y), 0x5410);
+        }
+    } else {
+        const auto pack = [](float a, float b) {
+            uint16_t r;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+            return (uint32_t)r;
+        };
+        w0 = pack(y[0].x, y[1].x);
+        w1 = pack(y[0].y, y[1].y);
+        if (N == 4) {
+            w0 |= pack(y[2].x, y[3].x) << 16;
+            w1 |= pack(y[2].y, y[3].y) << 16;
+        }
+    }
+}
+
 }  // namespace gdn2

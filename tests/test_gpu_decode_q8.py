@@ -258,3 +258,24 @@ def test_arguments_are_checked(g):
     with pytest.raises(g.Gdn2Error, match="n_tok"):
         e = _tokens(1, 9, 2, 2, 64, 64, torch.bfloat16, seed=16)
         g.gdn2_decode_multi_q8(*(e[k_] for k_ in NAMES), codes, scales)
+
+
+@pytest.mark.parametrize("n_tok", [1, 3])
+def test_loads_that_never_land_are_reported(g, n_tok):
+    """The loads withheld, the waits for them run out: nothing is written and the status word says so; the
+    next call works."""
+    d = _tokens(2, n_tok, 2, 2, 64, 64, torch.bfloat16, seed=17)
+    codes, scales = _pool(2, 2, 64, 64, torch.int8, seed=17)
+    c0, s0 = codes.clone(), scales.clone()
+    o = torch.full((2, n_tok, 2, 64), 123.0, device="cuda")
+    assert g.gdn2_device_status() == 0
+    lib = g.load_library()
+    lib.gdn2_testing_set_wait_limit(2_000_000, 1)
+    try:
+        g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, o=o)
+        assert g.gdn2_device_status() == g.GDN2_DEVICE_WAIT_TIMEOUT
+    finally:
+        lib.gdn2_testing_set_wait_limit(0, 0)
+    assert torch.all(o == 123.0) and torch.equal(codes, c0) and torch.equal(scales, s0)
+    g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, o=o)
+    assert g.gdn2_device_status() == 0 and not torch.any(o == 123.0)
