@@ -9,14 +9,14 @@
 // state stays in fp32 registers; only what is written to the pool, or to the per-token states, is
 // rounded.
 //
-// Persistent CTAs of 8 warps, two per SM, walk the (sequence, value head) items. One thread brings
-// the items two ahead into a ring of stages by bulk copies (codes, scales and token rows are
-// contiguous each), so HBM latency stays out of the way. Warp w owns key rows w DK / 8 ..; lane l
-// holds DV / 32 neighbouring columns of them. A row then lies in one warp: its largest magnitude is
-// one warp-wide reduction instruction, its factors are staged by the warp for itself, and its
-// codes leave as one 64- or 128-byte store. The two column sums cross the warps through shared
-// memory, which is the one barrier per token. Registers hold the state as pairs of rows: packed
-// two-wide arithmetic then takes the rows' factors as they lie in shared memory.
+// Persistent CTAs walk the (sequence, value head) items. The next items come into a ring of stages
+// by bulk copies (codes, scales and token rows are contiguous each), so HBM latency stays out of the
+// way. Warp w owns key rows w DK / W ..; lane l holds DV / 32 neighbouring columns of them. A row
+// then lies in one warp: its largest magnitude is one warp-wide reduction instruction, its factors
+// are staged by the warp for itself, and its codes leave as one 64- or 128-byte store. The two
+// column sums cross the warps through shared memory, which is the one barrier per token. The
+// arithmetic runs on pairs of rows: packed two-wide instructions take the rows' factors as they
+// lie in shared memory.
 #include "q8.cuh"
 #include "tc_ptx.cuh"
 
@@ -26,8 +26,6 @@ namespace {
 // Device status word of this file's kernels (kStatus* bits), read and cleared by
 // gdn2_device_status.
 __device__ unsigned int g_status_q8 = 0;
-
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -52,100 +50,135 @@ __device__ __forceinline__ float amax_nan(float a, float b, float c) {
     return d;
 }
 
-// One stage of the ring: codes, scales, and n_tok records [k, q, b, log_alpha or a, v, w].
-struct StageLayout {
-    int es, rec, rk, rq, rb, ra, rv, rw, bytes;
-    __host__ __device__ StageLayout(int dk, int dv, bool bf16, bool pro, int n_tok) {
-        es = bf16 ? 2 : 4;
-        rk = 0;
-        rq = dk * es;
-        rb = 2 * dk * es;
-        ra = 3 * dk * es;
-        rv = ra + dk * (pro ? es : 4);
-        rw = rv + dv * es;
-        rec = rw + dv * es;
-        bytes = dk * dv + dk * 4 + n_tok * rec;
+// Four neighbouring floats of shared memory as two pairs.
+__device__ __forceinline__ ulonglong2 pairs(const float* x) { return *reinterpret_cast<const ulonglong2*>(x); }
+
+// This lane's columns summed over the warps, as pairs of columns: partial sums of DK / 8 rows each, in
+// pairs first. With 4 warps the pairs have been added already, so both forms of the kernel
+// give the same bits.
+template <int CPL, int W, int DV>
+__device__ __forceinline__ void sum_warps(const float (&x)[W][DV], int c0, f32x2* s) {
+#pragma unroll
+    for (int w = 0; w < W; w += W / 4) {
+#pragma unroll
+        for (int j = 0; j < CPL / 2; ++j) {
+            f32x2 y = *reinterpret_cast<const f32x2*>(&x[w][c0 + 2 * j]);
+            if (W == 8) y = add2(y, *reinterpret_cast<const f32x2*>(&x[(w + 1) % W][c0 + 2 * j]));
+            s[j] = w == 0 ? y : add2(s[j], y);
+        }
     }
-};
+}
+template <int W>
+__device__ __forceinline__ float sum_dots(const float (&x)[W][4], int c) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; w += W / 4) {
+        const float y = W == 8 ? x[w][c] + x[(w + 1) % W][c] : x[w][c];
+        s = w == 0 ? y : s + y;
+    }
+    return s;
+}
 
 struct Ring {
     int stages, stage_bytes;
+    const void* src[8];  // what a stage is brought from: codes, scales, k, q, b, log_alpha or a, v, w
 };
 
-template <int DK, int DV, int kFmt, typename T, bool kPro>
-__global__ void __launch_bounds__(kThreads, 2) decode_q8_kernel(const __grid_constant__ Params p, const __grid_constant__ Q8Args a,
-                                                                const Ring ring) {
-    constexpr int RW = DK / kWarps, CPL = DV / 32;  // rows per warp, columns per lane
-    constexpr int kMaxStages = 3;
-    using W = typename Word<CPL>::type;
-    extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ __align__(16) float red[2][2][kWarps][DV];  // [token parity][r | p][warp][column]
-    __shared__ __align__(16) float dsum[2][kWarps][4];     // q . e, q . k, |q|^2, |k|^2 of a warp's rows
-    __shared__ __align__(16) float rows[kWarps][6][RW];  // k g, q g, g, k, -e; row maxima, then 1 / scale
-    __shared__ __align__(16) int4 head[kMaxStages];      // item (-1: no more), n, h, slot written
-    __shared__ __align__(8) uint64_t full[kMaxStages];
+// kOne: one token and no per-token states. Each warp then reads its codes twice, for the sums and
+// for the update, instead of holding 64 fp32 values a thread from one to the other: 4 CTAs of 4 warps
+// fit an SM, and the work that a warp does once per token is spread over twice the rows. Otherwise 2
+// CTAs of 8 warps, the state in registers from token to token.
+template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
+struct Cfg {
+    static constexpr int W = kOne ? 4 : 8, NT = 32 * W, CTAS = kOne ? 4 : 2;
+    static constexpr int RW = DK / W, CPL = DV / 32;       // rows per warp, columns per lane
+    static constexpr int G = RW < 16 ? RW : 16;            // rows quantised at a time
+    static constexpr int ES = sizeof(T), AB = kPro ? DK * ES : DK * 4;
+    static constexpr int RK = 0, RQ = DK * ES, RB = 2 * DK * ES, RA = 3 * DK * ES, RV = RA + AB, RWR = RV + DV * ES;
+    static constexpr int REC = RWR + DV * ES;              // one token's record in a stage
+    static constexpr int TOK = DK * DV + DK * 4;           // where the records start
+    static constexpr int MAX_STAGES = 3;
+};
 
-    const StageLayout L(DK, DV, sizeof(T) == 2, kPro, p.n_tok);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, n_tok = p.n_tok;
-    const int n_items = p.n_seq * p.h_v;
+template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
+__global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, DV, kFmt, T, kPro, kOne>::CTAS)
+    decode_q8_kernel(const __grid_constant__ Params p, const __grid_constant__ Q8Args a, const __grid_constant__ Ring ring) {
+    using C = Cfg<DK, DV, kFmt, T, kPro, kOne>;
+    constexpr int W = C::W, RW = C::RW, CPL = C::CPL, G = C::G, PR = DK / 8;  // PR: rows of a partial sum
+    using Wd = typename Word<CPL>::type;
+    extern __shared__ __align__(128) uint8_t dsm[];
+    __shared__ __align__(16) float red[2][2][W][DV];     // [token parity][r | p][warp][column]
+    __shared__ __align__(16) float dsum[2][W][4];        // q . e, q . k, |q|^2, |k|^2 of a warp's rows
+    __shared__ __align__(16) float rows[W][6][RW];       // k g, q g, g, k, -e; row maxima, then 1 / scale
+    __shared__ __align__(16) int4 head[C::MAX_STAGES];   // 0 (-1: no more items), n, h, slot written
+    __shared__ __align__(16) int4 next;                  // the next item to bring: item, slot, slot written
+    __shared__ __align__(8) int2 piece[8];               // bytes and place in the stage of the 8 copies
+    __shared__ __align__(8) uint64_t full[C::MAX_STAGES];
+    __shared__ int issued;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int n_tok = kOne ? 1 : p.n_tok, n_items = p.n_seq * p.h_v;
     const uint32_t full0 = tc::smem_u32(full), dsm0 = tc::smem_u32(dsm);
 
-    // ---- producer (thread 0): the next active item and its slots are known one issue ahead
-    int nit = blockIdx.x, nslot = -1, nout = -1, issued = 0;
-    bool ended = false;
-    auto look = [&]() {
-        for (; nit < n_items; nit += gridDim.x) {
-            const int n = nit / p.h_v;
-            nslot = p.slots ? p.slots[n] : n;
-            if (nslot >= 0 && nslot < p.n_slots) {
-                nout = a.slots_out ? a.slots_out[n] : nslot;
+    // Producer (warp 0). The next active item and its slots are looked up one issue ahead, and kept
+    // in shared memory: registers are what this kernel is short of.
+    auto look = [&](int it) {
+        int slot = -1, out = -1;
+        for (; it < n_items; it += gridDim.x) {
+            const int n = it / p.h_v;
+            slot = p.slots ? p.slots[n] : n;
+            if (slot >= 0 && slot < p.n_slots) {
+                out = a.slots_out ? a.slots_out[n] : slot;
                 break;
             }
         }
+        next = make_int4(it, slot, out, 0);
     };
-    auto issue = [&]() {
-        if (ended) return;
-        const int s = issued % ring.stages;
-        const uint32_t bar = full0 + 8 * s, dst = dsm0 + s * ring.stage_bytes;
-        ++issued;
-        if (nit >= n_items) {
-            ended = true;
-            head[s] = make_int4(-1, 0, 0, 0);
-            tc::mbar_arrive(bar);
-            return;
+    auto issue = [&](int i) {  // the i-th of this CTA
+        const int4 nx = next;
+        if (nx.x < 0) return;
+        const int s = i % ring.stages;
+        const uint32_t bar = full0 + 8 * s;
+        const bool none = nx.x >= n_items;
+        const int n = nx.x / p.h_v, h = nx.x % p.h_v;
+        if (lane == 0) {
+            issued = i + 1;
+            head[s] = make_int4(none ? -1 : 0, n, h, nx.z);
+            if (none) tc::mbar_arrive(bar);
+            else tc::mbar_expect_tx(bar, C::TOK + n_tok * C::REC);
         }
-        const int n = nit / p.h_v, h = nit % p.h_v, g = h / (p.h_v / p.h_qk);
-        head[s] = make_int4(nit, n, h, nout);
-        tc::mbar_expect_tx(bar, L.bytes);
-        const size_t st = (size_t)nslot * p.h_v + h;
-        bulk_load(dst, static_cast<const uint8_t*>(a.codes) + st * (DK * DV), DK * DV, bar);
-        bulk_load(dst + DK * DV, a.scales + st * DK, DK * 4, bar);
-        for (int t = 0; t < n_tok; ++t) {
-            const uint32_t rec = dst + DK * DV + DK * 4 + t * L.rec;
-            const size_t row = (size_t)n * n_tok + t, tq = (row * p.h_qk + g) * DK, tk = (row * p.h_v + h) * DK, tv = (row * p.h_v + h) * DV;
-            bulk_load(rec + L.rk, static_cast<const T*>(p.k) + tq, DK * sizeof(T), bar);
-            bulk_load(rec + L.rq, static_cast<const T*>(p.q) + tq, DK * sizeof(T), bar);
-            bulk_load(rec + L.rb, static_cast<const T*>(p.b) + tk, DK * sizeof(T), bar);
-            if (kPro)
-                bulk_load(rec + L.ra, static_cast<const T*>(p.a_raw) + tk, DK * sizeof(T), bar);
-            else
-                bulk_load(rec + L.ra, p.log_alpha + tk, DK * 4, bar);
-            bulk_load(rec + L.rv, static_cast<const T*>(p.v) + tv, DV * sizeof(T), bar);
-            bulk_load(rec + L.rw, static_cast<const T*>(p.w) + tv, DV * sizeof(T), bar);
+        __syncwarp();
+        if (!none && lane < 8) {  // lane c brings piece c
+            const int2 pc = piece[lane];
+            const size_t row = (size_t)n * n_tok;
+            const size_t idx = lane < 2 ? (size_t)nx.y * p.h_v + h : lane < 4 ? row * p.h_qk + h / (p.h_v / p.h_qk) : row * p.h_v + h;
+            const char* src = static_cast<const char*>(ring.src[lane]) + idx * pc.x;
+            uint32_t dst = dsm0 + s * ring.stage_bytes + pc.y;
+            const size_t step = (size_t)(lane < 4 ? p.h_qk : p.h_v) * pc.x;
+            bulk_load(dst, src, pc.x, bar);
+            if (!kOne && lane >= 2)
+                for (int t = 1; t < n_tok; ++t) bulk_load(dst += C::REC, src += step, pc.x, bar);
         }
-        nit += gridDim.x;
-        look();
+        if (lane == 0) {
+            if (none) next.x = -1;
+            else look(nx.x + gridDim.x);
+        }
+        __syncwarp();
     };
 
     if (tid == 0) {
         for (int s = 0; s < ring.stages; ++s) tc::mbar_init(full0 + 8 * s, 1);
         tc::fence_mbar_init();
+        issued = 0;
+        const int bytes[8] = {DK * DV, DK * 4, DK * C::ES, DK * C::ES, DK * C::ES, C::AB, DV * C::ES, DV * C::ES};
+        const int place[8] = {0, DK * DV, C::TOK + C::RK, C::TOK + C::RQ, C::TOK + C::RB, C::TOK + C::RA, C::TOK + C::RV, C::TOK + C::RWR};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) piece[c] = make_int2(bytes[c], place[c]);
+        look(blockIdx.x);
     }
     __syncthreads();
-    if (tid == 0 && !p.test_withhold_loads) {
-        look();
-        for (int s = 0; s + 1 < ring.stages; ++s) issue();
-    }
+    if (warp == 0 && !p.test_withhold_loads)
+        for (int s = 0; s + 1 < ring.stages; ++s) issue(s);
 
     float(*rv)[RW] = rows[warp];
     const int c0 = lane * CPL;
@@ -159,47 +192,50 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q8_kernel(const __grid_con
         const int4 hd = fault ? make_int4(0, 0, 0, -1) : head[st];
         if (hd.x < 0) break;
         const uint8_t* stage = dsm + st * ring.stage_bytes;
-        const float* scales = reinterpret_cast<const float*>(stage + DK * DV);
-        const uint8_t* rec = stage + DK * DV + DK * 4;
-
-        // this lane's columns of the warp's rows, as values of the codes, in pairs of rows
-        float2 v[RW / 2][CPL];
+        const uint8_t* mine = stage + warp * (RW * DV) + c0;  // this lane's columns of the warp's rows
+        const uint8_t* rec = stage + C::TOK;
+        // values of the codes of rows 2i and 2i + 1, as pairs
+        auto values = [&](int i, f32x2* x) {
+            q8_unpack_pair<kFmt, CPL>(*reinterpret_cast<const Wd*>(mine + 2 * i * DV), *reinterpret_cast<const Wd*>(mine + (2 * i + 1) * DV), x);
+        };
+        f32x2 v[kOne ? G / 2 : RW / 2][CPL];
+        if (!kOne) {
 #pragma unroll
-        for (int i = 0; i < RW / 2; ++i) {
-            const uint8_t* at = stage + (size_t)(warp * RW + 2 * i) * DV + c0;
-            q8_unpack_pair<kFmt, CPL>(*reinterpret_cast<const W*>(at), *reinterpret_cast<const W*>(at + DV), v[i]);
+            for (int i = 0; i < RW / 2; ++i) values(i, v[i]);
         }
-        for (int t = 0; t < n_tok; ++t, rec += L.rec, buf ^= 1) {
+        for (int t = 0; t < n_tok; ++t, rec += C::REC, buf ^= 1) {
             // the warp's row factors
             __syncwarp();
             float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-            if (lane < RW) {
+            if (RW == 32 || lane < RW) {
                 const int i = warp * RW + lane;
-                const float kv = to_f32(reinterpret_cast<const T*>(rec + L.rk)[i]), qv = to_f32(reinterpret_cast<const T*>(rec + L.rq)[i]);
-                float bv = to_f32(reinterpret_cast<const T*>(rec + L.rb)[i]);
+                const float kv = to_f32(reinterpret_cast<const T*>(rec + C::RK)[i]), qv = to_f32(reinterpret_cast<const T*>(rec + C::RQ)[i]);
+                float bv = to_f32(reinterpret_cast<const T*>(rec + C::RB)[i]);
                 float g;
                 if (kPro) {
-                    g = sigmoid_f(-to_f32(reinterpret_cast<const T*>(rec + L.ra)[i]));
+                    g = sigmoid_f(-to_f32(reinterpret_cast<const T*>(rec + C::RA)[i]));
                     bv = sigmoid_f(bv);
                 } else {
-                    g = expf(reinterpret_cast<const float*>(rec + L.ra)[i]);
+                    g = expf(reinterpret_cast<const float*>(rec + C::RA)[i]);
                 }
-                if (t == 0) g *= scales[i];
+                if (t == 0) g *= reinterpret_cast<const float*>(stage + DK * DV)[i];
                 const float e = bv * kv;
                 rv[0][lane] = kv * g;
                 rv[1][lane] = qv * g;
                 rv[2][lane] = g;
                 rv[3][lane] = kv;
                 rv[4][lane] = -e;
-                d0 = qv * e;
-                d1 = qv * kv;
+                // __fmul_rn: not contracted with the sums below, so that all forms round alike
+                d0 = __fmul_rn(qv, e);
+                d1 = __fmul_rn(qv, kv);
                 if (kPro) {
-                    d2 = qv * qv;
-                    d3 = kv * kv;
+                    d2 = __fmul_rn(qv, qv);
+                    d3 = __fmul_rn(kv, kv);
                 }
             }
 #pragma unroll
-            for (int off = RW / 2; off > 0; off >>= 1) {
+            for (int s_ = 0; (1 << s_) < RW; ++s_) {  // within a partial sum's rows, then over its two
+                const int off = (1 << s_) < PR ? (PR / 2) >> s_ : PR;
                 d0 += __shfl_xor_sync(0xffffffffu, d0, off);
                 d1 += __shfl_xor_sync(0xffffffffu, d1, off);
                 if (kPro) {
@@ -210,25 +246,32 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q8_kernel(const __grid_con
             if (lane == 0) *reinterpret_cast<float4*>(dsum[buf][warp]) = make_float4(d0, d1, d2, d3);
             __syncwarp();
 
-            float2 r2[CPL], p2[CPL];
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) r2[j] = p2[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < RW / 4; ++i) {
-                const float4 kg = *reinterpret_cast<const float4*>(&rv[0][4 * i]), qg = *reinterpret_cast<const float4*>(&rv[1][4 * i]);
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    r2[j] = ffma2(make_float2(kg.x, kg.y), v[2 * i][j], r2[j]);
-                    p2[j] = ffma2(make_float2(qg.x, qg.y), v[2 * i][j], p2[j]);
-                    r2[j] = ffma2(make_float2(kg.z, kg.w), v[2 * i + 1][j], r2[j]);
-                    p2[j] = ffma2(make_float2(qg.z, qg.w), v[2 * i + 1][j], p2[j]);
-                }
-            }
+            f32x2 r2[CPL], p2[CPL];
             Cols<float, CPL> rs, ps;
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                rs.x[j] = r2[j].x + r2[j].y;
-                ps.x[j] = p2[j].x + p2[j].y;
+            for (int i = 0; i < RW / 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < CPL; ++j)
+                    if (i % (PR / 4) == 0) r2[j] = p2[j] = 0ull;
+                const ulonglong2 kg = pairs(&rv[0][4 * i]), qg = pairs(&rv[1][4 * i]);
+                f32x2 y[2][CPL];
+                if (kOne) {
+                    values(2 * i, y[0]);
+                    values(2 * i + 1, y[1]);
+                }
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    const f32x2 y0 = kOne ? y[0][j] : v[(2 * i) % (RW / 2)][j], y1 = kOne ? y[1][j] : v[(2 * i + 1) % (RW / 2)][j];
+                    r2[j] = fma2(kg.x, y0, r2[j]);
+                    p2[j] = fma2(qg.x, y0, p2[j]);
+                    r2[j] = fma2(kg.y, y1, r2[j]);
+                    p2[j] = fma2(qg.y, y1, p2[j]);
+                    if (i % (PR / 4) == PR / 4 - 1) {
+                        const float2 ra = unpack2(r2[j]), pa = unpack2(p2[j]);
+                        rs.x[j] = i < PR / 4 ? ra.x + ra.y : rs.x[j] + (ra.x + ra.y);
+                        ps.x[j] = i < PR / 4 ? pa.x + pa.y : ps.x[j] + (pa.x + pa.y);
+                    }
+                }
             }
             *reinterpret_cast<Cols<float, CPL>*>(&red[buf][0][warp][c0]) = rs;
             *reinterpret_cast<Cols<float, CPL>*>(&red[buf][1][warp][c0]) = ps;
@@ -237,111 +280,125 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q8_kernel(const __grid_con
                 fault = true;
                 break;
             }
-            if (t == 0 && tid == 0) issue();
-            float r[CPL];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const Cols<float, CPL> y = *reinterpret_cast<const Cols<float, CPL>*>(&red[buf][0][w][c0]);
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) r[j] = w == 0 ? y.x[j] : r[j] + y.x[j];
-            }
+            if (t == 0 && warp == 0) issue(taken + ring.stages - 1);
+            f32x2 rc[CPL / 2];
+            sum_warps<CPL>(red[buf][0], c0, rc);
             // fused pre-processing: q and k enter unnormalised, and each sum takes its norms here
             float nq = 1.f, nk = 1.f;
             if (kPro) {
-                float sq = 0.f, sk = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    sq += dsum[buf][w][2];
-                    sk += dsum[buf][w][3];
-                }
-                nq = 1.f / fmaxf(sqrtf(sq), kL2NormEps);
-                nk = 1.f / fmaxf(sqrtf(sk), kL2NormEps);
+                nq = 1.f / fmaxf(sqrtf(sum_dots(dsum[buf], 2)), kL2NormEps);
+                nk = 1.f / fmaxf(sqrtf(sum_dots(dsum[buf], 3)), kL2NormEps);
             }
-            const T *tv = reinterpret_cast<const T*>(rec + L.rv), *tw = reinterpret_cast<const T*>(rec + L.rw);
-            auto write = [](T w, T v_t) { return (kPro ? sigmoid_f(to_f32(w)) : to_f32(w)) * to_f32(v_t); };  // x = w (.) v
             const size_t row = ((size_t)hd.y * n_tok + t) * p.h_v + hd.z;
-            if (tid < DV) {
-                float pj = 0.f, rj = 0.f, qe = 0.f, qk = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    rj += red[buf][0][w][tid];
-                    pj += red[buf][1][w][tid];
-                    qe += dsum[buf][w][0];
-                    qk += dsum[buf][w][1];
-                }
-                const float o = nq * (pj + nk * (qk * write(tw[tid], tv[tid]) - qe * (nk * rj)));
-                if (a.o_bf16)
-                    static_cast<__nv_bfloat16*>(p.o)[row * DV + tid] = __float2bfloat16_rn(o);
-                else
-                    static_cast<float*>(p.o)[row * DV + tid] = o;
-            }
-            float x[CPL];
-            const Cols<T, CPL> wc = *reinterpret_cast<const Cols<T, CPL>*>(tw + c0), vc = *reinterpret_cast<const Cols<T, CPL>*>(tv + c0);
+            const Cols<T, CPL> wc = reinterpret_cast<const Cols<T, CPL>*>(rec + C::RWR)[lane], vc = reinterpret_cast<const Cols<T, CPL>*>(rec + C::RV)[lane];
+            float x[CPL], r[CPL];
 #pragma unroll
             for (int j = 0; j < CPL; ++j) {
-                x[j] = nk * write(wc.x[j], vc.x[j]);
-                r[j] *= nk * nk;
+                const float2 rr = unpack2(rc[j / 2]);
+                const float wv = to_f32(wc.x[j]);
+                x[j] = nk * ((kPro ? sigmoid_f(wv) : wv) * to_f32(vc.x[j]));
+                r[j] = nk * (j % 2 ? rr.y : rr.x);
             }
-#pragma unroll
-            for (int i = 0; i < RW / 4; ++i) {
-                const float4 g4 = *reinterpret_cast<const float4*>(&rv[2][4 * i]), k4 = *reinterpret_cast<const float4*>(&rv[3][4 * i]);
-                const float4 e4 = *reinterpret_cast<const float4*>(&rv[4][4 * i]);
+            if (warp == ((taken + t) & (W - 1))) {  // one warp, another each time, writes the outputs
+                f32x2 pc[CPL / 2];
+                sum_warps<CPL>(red[buf][1], c0, pc);
+                const float qe = sum_dots(dsum[buf], 0), qk = sum_dots(dsum[buf], 1);
+                float o[CPL];
 #pragma unroll
                 for (int j = 0; j < CPL; ++j) {
-                    v[2 * i][j] = ffma2(make_float2(g4.x, g4.y), v[2 * i][j],
-                                        ffma2(make_float2(k4.x, k4.y), dup2(x[j]), fmul2(make_float2(e4.x, e4.y), dup2(r[j]))));
-                    v[2 * i + 1][j] = ffma2(make_float2(g4.z, g4.w), v[2 * i + 1][j],
-                                            ffma2(make_float2(k4.z, k4.w), dup2(x[j]), fmul2(make_float2(e4.z, e4.w), dup2(r[j]))));
+                    const float2 pp = unpack2(pc[j / 2]);
+                    o[j] = __fmul_rn(nq, fmaf(qk, x[j], fmaf(-__fmul_rn(nk, qe), r[j], j % 2 ? pp.y : pp.x)));
                 }
-            }
-            const bool last = t + 1 == n_tok;
-            if (!last && !a.code_steps) continue;
-
-            // quantise: the row maxima, then one row's scale per lane
-            float m[RW];
+                if (a.o_bf16) {
+                    Cols<__nv_bfloat16, CPL> ob;
 #pragma unroll
-            for (int i = 0; i < RW / 2; ++i) {
-                if (CPL == 4) {
-                    m[2 * i] = amax_nan(amax_nan(v[i][0].x, v[i][1].x, v[i][2 % CPL].x), v[i][3 % CPL].x);
-                    m[2 * i + 1] = amax_nan(amax_nan(v[i][0].y, v[i][1].y, v[i][2 % CPL].y), v[i][3 % CPL].y);
+                    for (int j = 0; j < CPL; ++j) ob.x[j] = __float2bfloat16_rn(o[j]);
+                    *reinterpret_cast<Cols<__nv_bfloat16, CPL>*>(static_cast<__nv_bfloat16*>(p.o) + row * DV + c0) = ob;
                 } else {
-                    m[2 * i] = amax_nan(v[i][0].x, v[i][1].x);
-                    m[2 * i + 1] = amax_nan(v[i][0].y, v[i][1].y);
+                    Cols<float, CPL> of;
+#pragma unroll
+                    for (int j = 0; j < CPL; ++j) of.x[j] = o[j];
+                    *reinterpret_cast<Cols<float, CPL>*>(static_cast<float*>(p.o) + row * DV + c0) = of;
                 }
             }
+            const bool last = t + 1 == n_tok, keep = last && hd.w >= 0 && hd.w < p.n_slots;
+            f32x2 xx[CPL], rr[CPL];
 #pragma unroll
-            for (int i = 0; i < RW; ++i) m[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[i])));
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < RW / 4; ++i) *reinterpret_cast<float4*>(&rv[5][4 * i]) = make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+            for (int j = 0; j < CPL; ++j) {
+                xx[j] = pack2(x[j], x[j]);
+                rr[j] = pack2(nk * r[j], nk * r[j]);
             }
-            __syncwarp();
-            float scale = 0.f, inv = 1.f;
-            if (lane < RW) {
-                q8_scale<kFmt>(rv[5][lane], scale, inv);
-                rv[5][lane] = inv;
-            }
-            __syncwarp();
-            const bool zero_rows = __any_sync(0xffffffffu, inv == 0.f);
-            uint32_t word[RW];
+            // the new state, G rows at a time
+            constexpr int kPasses = RW / G;
+#pragma unroll 1
+            for (int ps_ = 0; ps_ < kPasses; ++ps_) {
+                const int i0 = ps_ * G;
 #pragma unroll
-            for (int i = 0; i < RW / 4; ++i) {
-                const float4 i4 = *reinterpret_cast<const float4*>(&rv[5][4 * i]);
-                q8_pack_pair<kFmt, CPL>(v[2 * i], make_float2(i4.x, i4.y), word[4 * i], word[4 * i + 1]);
-                q8_pack_pair<kFmt, CPL>(v[2 * i + 1], make_float2(i4.z, i4.w), word[4 * i + 2], word[4 * i + 3]);
-            }
-            if (zero_rows) {  // rows whose codes are 0 whatever they hold
+                for (int i = 0; i < G / 4; ++i) {
+                    const ulonglong2 g4 = pairs(&rv[2][i0 + 4 * i]), k4 = pairs(&rv[3][i0 + 4 * i]), e4 = pairs(&rv[4][i0 + 4 * i]);
+                    if (kOne) {
+                        values(i0 / 2 + 2 * i, v[2 * i]);
+                        values(i0 / 2 + 2 * i + 1, v[2 * i + 1]);
+                    }
 #pragma unroll
-                for (int i = 0; i < RW; ++i) word[i] = rv[5][i] == 0.f ? 0u : word[i];
-            }
-            auto put = [&](void* codes, float* sc, size_t state) {
-                uint8_t* at = static_cast<uint8_t*>(codes) + state * (DK * DV) + (size_t)warp * RW * DV + c0;
+                    for (int j = 0; j < CPL; ++j) {
+                        v[2 * i][j] = fma2(g4.x, v[2 * i][j], fma2(k4.x, xx[j], mul2(e4.x, rr[j])));
+                        v[2 * i + 1][j] = fma2(g4.y, v[2 * i + 1][j], fma2(k4.y, xx[j], mul2(e4.y, rr[j])));
+                    }
+                }
+                if (kOne ? !keep : !(keep || a.code_steps)) continue;
+
+                // quantise: the row maxima, then one row's scale per lane
+                float m[G];
 #pragma unroll
-                for (int i = 0; i < RW; ++i) *reinterpret_cast<W*>(at + i * DV) = (W)word[i];
-                if (lane < RW) sc[state * DK + warp * RW + lane] = scale;
-            };
-            if (a.code_steps) put(a.code_steps, a.scale_steps, row);
-            if (last && hd.w >= 0 && hd.w < p.n_slots) put(a.codes, a.scales, (size_t)hd.w * p.h_v + hd.z);
+                for (int i = 0; i < G / 2; ++i) {
+                    float2 y[CPL];
+#pragma unroll
+                    for (int j = 0; j < CPL; ++j) y[j] = unpack2(v[i][j]);
+                    if (CPL == 4) {
+                        m[2 * i] = amax_nan(amax_nan(y[0].x, y[1].x, y[2 % CPL].x), y[3 % CPL].x);
+                        m[2 * i + 1] = amax_nan(amax_nan(y[0].y, y[1].y, y[2 % CPL].y), y[3 % CPL].y);
+                    } else {
+                        m[2 * i] = amax_nan(y[0].x, y[1].x);
+                        m[2 * i + 1] = amax_nan(y[0].y, y[1].y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < G; ++i) m[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[i])));
+                if (lane == 0) {
+#pragma unroll
+                    for (int i = 0; i < G / 4; ++i)
+                        *reinterpret_cast<float4*>(&rv[5][i0 + 4 * i]) = make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+                }
+                __syncwarp();
+                float scale = 0.f, inv = 1.f;
+                if (lane < G) {
+                    q8_scale<kFmt>(rv[5][i0 + lane], scale, inv);
+                    rv[5][i0 + lane] = inv;
+                }
+                __syncwarp();
+                const bool zero_rows = __any_sync(0xffffffffu, inv == 0.f);
+                uint32_t word[G];
+#pragma unroll
+                for (int i = 0; i < G / 4; ++i) {
+                    const ulonglong2 i4 = pairs(&rv[5][i0 + 4 * i]);
+                    q8_pack_pair<kFmt, CPL>(v[2 * i], i4.x, word[4 * i], word[4 * i + 1]);
+                    q8_pack_pair<kFmt, CPL>(v[2 * i + 1], i4.y, word[4 * i + 2], word[4 * i + 3]);
+                }
+                if (zero_rows) {  // rows whose codes are 0 whatever they hold
+#pragma unroll
+                    for (int i = 0; i < G; ++i) word[i] = rv[5][i0 + i] == 0.f ? 0u : word[i];
+                }
+                auto put = [&](void* codes, float* sc, size_t state) {
+                    const size_t r0 = state * DK + warp * RW + i0;
+                    uint8_t* at = static_cast<uint8_t*>(codes) + r0 * DV + c0;
+#pragma unroll
+                    for (int i = 0; i < G; ++i) *reinterpret_cast<Wd*>(at + i * DV) = (Wd)word[i];
+                    if (lane < G) sc[r0 + lane] = scale;
+                };
+                if (!kOne && a.code_steps) put(a.code_steps, a.scale_steps, row);
+                if (keep) put(a.codes, a.scales, (size_t)hd.w * p.h_v + hd.z);
+            }
         }
         if (fault) break;
     }
@@ -352,32 +409,37 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q8_kernel(const __grid_con
     }
 }
 
-template <int DK, int DV, int kFmt, typename T, bool kPro>
+template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
 cudaError_t launch(const Params& p, const Q8Args& a, cudaStream_t st) {
-    auto kern = decode_q8_kernel<DK, DV, kFmt, T, kPro>;
-    const StageLayout L(DK, DV, sizeof(T) == 2, kPro, p.n_tok);
-    Ring ring;
-    ring.stage_bytes = (L.bytes + 127) & ~127;
-    // three stages (two items ahead) where two CTAs of them fit an SM, else two
-    ring.stages = 3 * ring.stage_bytes <= 90 * 1024 ? 3 : 2;
+    using C = Cfg<DK, DV, kFmt, T, kPro, kOne>;
+    auto kern = decode_q8_kernel<DK, DV, kFmt, T, kPro, kOne>;
+    Ring ring{0, (C::TOK + p.n_tok * C::REC + 127) & ~127,
+              {a.codes, a.scales, p.k, p.q, p.b, kPro ? p.a_raw : static_cast<const void*>(p.log_alpha), p.v, p.w}};
+    // three stages (two items ahead) where the SM's CTAs have room for them, else two
+    ring.stages = C::CTAS * (3 * ring.stage_bytes + 22 * 1024) <= 224 * 1024 ? 3 : 2;
     const int smem = ring.stages * ring.stage_bytes;
     int dev = 0, sms = 0, per_sm = 0;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::NT, smem);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     const int items = p.n_seq * p.h_v;
-    kern<<<items < sms * per_sm ? items : sms * per_sm, kThreads, smem, st>>>(p, a, ring);
+    kern<<<items < sms * per_sm ? items : sms * per_sm, C::NT, smem, st>>>(p, a, ring);
     return cudaGetLastError();
+}
+
+template <int DK, int DV, int kFmt, typename T, bool kPro>
+cudaError_t launch_n(const Params& p, const Q8Args& a, cudaStream_t st) {
+    return p.n_tok == 1 && !a.code_steps ? launch<DK, DV, kFmt, T, kPro, true>(p, a, st) : launch<DK, DV, kFmt, T, kPro, false>(p, a, st);
 }
 
 template <int DK, int DV, int kFmt>
 cudaError_t launch_t(const Params& p, const Q8Args& a, cudaStream_t st) {
-    if (a.bf16) return p.prologue ? launch<DK, DV, kFmt, __nv_bfloat16, true>(p, a, st) : launch<DK, DV, kFmt, __nv_bfloat16, false>(p, a, st);
-    return p.prologue ? launch<DK, DV, kFmt, float, true>(p, a, st) : launch<DK, DV, kFmt, float, false>(p, a, st);
+    if (a.bf16) return p.prologue ? launch_n<DK, DV, kFmt, __nv_bfloat16, true>(p, a, st) : launch_n<DK, DV, kFmt, __nv_bfloat16, false>(p, a, st);
+    return p.prologue ? launch_n<DK, DV, kFmt, float, true>(p, a, st) : launch_n<DK, DV, kFmt, float, false>(p, a, st);
 }
 
 template <int kFmt>

@@ -37,6 +37,25 @@ __device__ __forceinline__ void q8_scale(float amax, float& scale, float& inv) {
 // Magnitudes are compared as integers: ordered like the values, and an infinity or a NaN wins.
 __device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// Four values as e4m3 bytes and back (e4m3 is exact in fp16, and fp16 in fp32).
+__device__ __forceinline__ uint32_t e4m3x4(float4 x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w));
+    return r;
+}
+__device__ __forceinline__ float4 e4m3x4_values(uint32_t c) {
+    float4 x;
+    asm("{\n\t.reg .b16 l, h, a, b, c, d;\n\t.reg .b32 p, q;\n\tmov.b32 {l, h}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\tmov.b32 {a, b}, p;\n\tmov.b32 {c, d}, q;\n\t"
+        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\tcvt.f32.f16 %2, c;\n\tcvt.f32.f16 %3, d;\n\t}"
+        : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+        : "r"(c));
+    return x;
+}
+
 // Four codes of x * inv, packed in column order.
 template <int kFmt>
 __device__ __forceinline__ uint32_t q8_pack(float4 x, float inv) {
@@ -50,10 +69,7 @@ __device__ __forceinline__ uint32_t q8_pack(float4 x, float inv) {
         const uint32_t d = __float_as_uint(__fadd_rn(x.z, c)), e = __float_as_uint(__fadd_rn(x.w, c));
         r = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
     } else {
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y), "f"(x.x));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x.w), "f"(x.z));
-        r = (uint32_t)lo | ((uint32_t)hi << 16);
+        r = e4m3x4(x);
     }
     return inv == 0.f ? 0u : r;
 }
@@ -70,48 +86,71 @@ __device__ __forceinline__ float4 q8_unpack(uint32_t c) {
                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7652)) - m,
                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7653)) - m);
     } else {
-        uint32_t lo, hi;  // e4m3 is exact in fp16, and fp16 in fp32
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(c & 0xffffu)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(c >> 16)));
-        float4 x;
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(x.x), "=f"(x.y) : "r"(lo));
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(x.z), "=f"(x.w) : "r"(hi));
-        return x;
+        return e4m3x4_values(c);
     }
 }
 
-// The same for two rows at once, as pairs (row 0, row 1) per column; N columns in the low bytes of
+// Two fp32 values in one 64-bit register, for packed arithmetic without moves between registers.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 d) {
+    float2 x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(d));
+    return x;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// q8_unpack for two rows at once, as pairs (row 0, row 1) per column; N columns in the low bytes of
 // each row's word.
 template <int kFmt, int N>
-__device__ __forceinline__ void q8_unpack_pair(uint32_t w0, uint32_t w1, float2* x) {
+__device__ __forceinline__ void q8_unpack_pair(uint32_t w0, uint32_t w1, f32x2* x) {
     if (kFmt == GDN2_Q8_INT8) {
         const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
-        const float2 m = make_float2(-8388736.f, -8388736.f);
+        const f32x2 m = pack2(-8388736.f, -8388736.f);
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            x[j] = fadd2(make_float2(__uint_as_float(__byte_perm(u0, 0x4b000000u, 0x7650 | j)),
-                                     __uint_as_float(__byte_perm(u1, 0x4b000000u, 0x7650 | j))), m);
+            x[j] = add2(pack2(__uint_as_float(__byte_perm(u0, 0x4b000000u, 0x7650 | j)),
+                              __uint_as_float(__byte_perm(u1, 0x4b000000u, 0x7650 | j))), m);
     } else {
         const float4 a = q8_unpack<kFmt>(w0), b = q8_unpack<kFmt>(w1);
-        x[0] = make_float2(a.x, b.x);
-        x[1] = make_float2(a.y, b.y);
+        x[0] = pack2(a.x, b.x);
+        x[1] = pack2(a.y, b.y);
         if (N == 4) {
-            x[2 % N] = make_float2(a.z, b.z);
-            x[3 % N] = make_float2(a.w, b.w);
+            x[2 % N] = pack2(a.z, b.z);
+            x[3 % N] = pack2(a.w, b.w);
         }
     }
 }
 
 // Codes of two rows' values, inv = (row 0's, row 1's), without q8_pack's rule for inv = 0.
 template <int kFmt, int N>
-__device__ __forceinline__ void q8_pack_pair(const float2* x, float2 inv, uint32_t& w0, uint32_t& w1) {
+__device__ __forceinline__ void q8_pack_pair(const f32x2* x, f32x2 inv, uint32_t& w0, uint32_t& w1) {
     float2 y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = j < N ? fmul2(x[j % N], inv) : make_float2(0.f, 0.f);
+    for (int j = 0; j < 4; ++j) {
+        f32x2 z = j < N ? mul2(x[j % N], inv) : 0ull;
+        if (kFmt == GDN2_Q8_INT8 && j < N) z = add2(z, pack2(12582912.f, 12582912.f));
+        y[j] = unpack2(z);
+    }
     if (kFmt == GDN2_Q8_INT8) {
-        const float2 c = make_float2(12582912.f, 12582912.f);
-#pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = fadd2(y[j], c);
         const auto pack = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040); };
         w0 = pack(y[0].x, y[1].x);
         w1 = pack(y[0].y, y[1].y);
@@ -120,17 +159,8 @@ __device__ __forceinline__ void q8_pack_pair(const float2* x, float2 inv, uint32
             w1 = __byte_perm(w1, pack(y[2].y, y[3].y), 0x5410);
         }
     } else {
-        const auto pack = [](float a, float b) {
-            uint16_t r;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-            return (uint32_t)r;
-        };
-        w0 = pack(y[0].x, y[1].x);
-        w1 = pack(y[0].y, y[1].y);
-        if (N == 4) {
-            w0 |= pack(y[2].x, y[3].x) << 16;
-            w1 |= pack(y[2].y, y[3].y) << 16;
-        }
+        w0 = e4m3x4(make_float4(y[0].x, y[1].x, y[2].x, y[3].x));
+        w1 = e4m3x4(make_float4(y[0].y, y[1].y, y[2].y, y[3].y));
     }
 }
 
