@@ -84,10 +84,10 @@ struct Ring {
     const void* src[8];  // what a stage is brought from: codes, scales, k, q, b, log_alpha or a, v, w
 };
 
-// kOne: one token and no per-token states. Each warp then reads its codes twice, for the sums and
-// for the update, instead of holding 64 fp32 values a thread from one to the other: 4 CTAs of 4 warps
-// fit an SM, and the work that a warp does once per token is spread over twice the rows. Otherwise 2
-// CTAs of 8 warps, the state in registers from token to token.
+// kOne: one token and no per-token states. 4 CTAs of 4 warps then fit an SM, and the work that a
+// warp does once per token is spread over twice the rows: a thread keeps the values of one half of its
+// rows from the sums to the update, and reads the other half's codes again. Otherwise 2 CTAs of 8
+// warps, the state in registers from token to token.
 template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
 struct Cfg {
     static constexpr int W = kOne ? 4 : 8, NT = 32 * W, CTAS = kOne ? 4 : 2;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, 
         auto values = [&](int i, f32x2* x) {
             q8_unpack_pair<kFmt, CPL>(*reinterpret_cast<const Wd*>(mine + 2 * i * DV), *reinterpret_cast<const Wd*>(mine + (2 * i + 1) * DV), x);
         };
-        f32x2 v[kOne ? G / 2 : RW / 2][CPL];
+        f32x2 v[G / 2][CPL];
         if (!kOne) {
 #pragma unroll
             for (int i = 0; i < RW / 2; ++i) values(i, v[i]);
@@ -255,13 +255,17 @@ __global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, 
                     if (i % (PR / 4) == 0) r2[j] = p2[j] = 0ull;
                 const ulonglong2 kg = pairs(&rv[0][4 * i]), qg = pairs(&rv[1][4 * i]);
                 f32x2 y[2][CPL];
-                if (kOne) {
+                if (i < RW / 4 - G / 4) {
                     values(2 * i, y[0]);
                     values(2 * i + 1, y[1]);
+                } else if (kOne) {  // the last G rows stay in registers
+                    values(2 * i, v[(2 * i) % (G / 2)]);
+                    values(2 * i + 1, v[(2 * i + 1) % (G / 2)]);
                 }
 #pragma unroll
                 for (int j = 0; j < CPL; ++j) {
-                    const f32x2 y0 = kOne ? y[0][j] : v[(2 * i) % (RW / 2)][j], y1 = kOne ? y[1][j] : v[(2 * i + 1) % (RW / 2)][j];
+                    const bool kept = i >= RW / 4 - G / 4;
+                    const f32x2 y0 = kept ? v[(2 * i) % (G / 2)][j] : y[0][j], y1 = kept ? v[(2 * i + 1) % (G / 2)][j] : y[1][j];
                     r2[j] = fma2(kg.x, y0, r2[j]);
                     p2[j] = fma2(qg.x, y0, p2[j]);
                     r2[j] = fma2(kg.y, y1, r2[j]);
@@ -332,11 +336,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, 
             constexpr int kPasses = RW / G;
 #pragma unroll 1
             for (int ps_ = 0; ps_ < kPasses; ++ps_) {
-                const int i0 = ps_ * G;
+                const int i0 = (kPasses - 1 - ps_) * G;
 #pragma unroll
                 for (int i = 0; i < G / 4; ++i) {
                     const ulonglong2 g4 = pairs(&rv[2][i0 + 4 * i]), k4 = pairs(&rv[3][i0 + 4 * i]), e4 = pairs(&rv[4][i0 + 4 * i]);
-                    if (kOne) {
+                    if (kPasses > 1 && ps_ > 0) {
                         values(i0 / 2 + 2 * i, v[2 * i]);
                         values(i0 / 2 + 2 * i + 1, v[2 * i + 1]);
                     }

@@ -24,14 +24,31 @@ template <int kFmt> struct Q8;
 template <> struct Q8<GDN2_Q8_INT8> { static constexpr float kTop = 127.f; };
 template <> struct Q8<GDN2_Q8_E4M3> { static constexpr float kTop = 448.f; };
 
-// Scale and inverse of a row from the bits of its largest magnitude; inv = 0 marks a row whose
-// codes are 0.
+// Scale and inverse of a row from its largest magnitude; inv = 0 marks a row whose codes are 0.
+//
+// Both quotients are rounded to nearest by a fused multiply-add on the remainder of a first
+// quotient (Markstein 1990): with y close to 1 / d, q = fl(n y) and the exact remainder
+// r = n - q d, fl(q + r y) is the rounded quotient. For a / M, 1 / M is a rounded constant. For
+// M / a, a's mantissa m in [1, 2) is divided by, with y from one Newton step on the hardware's
+// approximate reciprocal, and the exponent subtracted after it, so nothing over- or underflows for any
+// a from 2^-100 up. There are 2^23 mantissas: all of them were compared with __fdiv_rn (the test
+// of the stored scales and codes covers them again).
 template <int kFmt>
 __device__ __forceinline__ void q8_scale(float amax, float& scale, float& inv) {
-    const bool finite = __float_as_uint(amax) < 0x7f800000u;
-    const bool keep = finite && amax >= kQ8Tiny;
-    scale = keep ? __fdiv_rn(amax, Q8<kFmt>::kTop) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
-    inv = keep ? __fdiv_rn(Q8<kFmt>::kTop, amax) : 0.f;
+    constexpr float M = Q8<kFmt>::kTop, yM = 1.f / M;
+    const uint32_t bits = __float_as_uint(amax);
+    const float m = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m));
+    y = fmaf(y, fmaf(-m, y, 1.f), y);
+    float q = __fmul_rn(M, y);
+    q = fmaf(fmaf(-m, q, M), y, q);
+    inv = __uint_as_float(__float_as_uint(q) - (bits & 0x7f800000u) + 0x3f800000u);
+    const float s = __fmul_rn(amax, yM);
+    scale = fmaf(fmaf(-M, s, amax), yM, s);
+    const bool finite = bits < 0x7f800000u, keep = finite && amax >= kQ8Tiny;
+    scale = keep ? scale : finite ? 0.f : __uint_as_float(0x7fc00000u);
+    inv = keep ? inv : 0.f;
 }
 
 // Magnitudes are compared as integers: ordered like the values, and an infinity or a NaN wins.

@@ -88,6 +88,27 @@ def test_special_rows(g, dtype):
 
 
 @pytest.mark.parametrize("dtype", FORMATS)
+def test_scale_of_every_mantissa(g, dtype):
+    """The scale a / M is correctly rounded for each of the 2^23 mantissas that a can have, at three
+    exponents, and the inverse M / a shows in the codes of a row's other values."""
+    top = R.TOP[dtype]
+    codes = torch.zeros(1024, 16, 128, 64, dtype=dtype, device="cuda")
+    scales = torch.zeros(1024, 16, 128, device="cuda")
+    part = 2 ** 21
+    col = torch.linspace(0.001, 0.999, 64, device="cuda")
+    col[5] = 1.0
+    for exponent in (28, 127, 254):
+        for first in range(0, 2 ** 23, part):
+            a = ((exponent << 23) + first + torch.arange(part, dtype=torch.int32, device="cuda")).view(torch.float32)
+            S = (a[:, None] * col).view(1024, 16, 128, 64)
+            g.gdn2_state_store(S, codes, scales)
+            m = torch.full_like(a, top)  # a tensor: by a number, torch multiplies with a rounded inverse
+            assert torch.equal(scales.view(-1), a / m)
+            want = S.view(-1, 64) * (m / a)[:, None]
+            assert torch.equal(codes.view(-1, 64).float(), want.round() if dtype == torch.int8 else want.to(dtype).float())
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
 def test_slots_skipped_shared_and_absent(g, dtype):
     n, h, d = 4, 2, 64
     S = _states(n, h, d, d, seed=4)
