@@ -144,9 +144,6 @@ def _expect(name, t, shape, dtype=None, device=None, optional=False):
     """Argument check before any launch: the kernels take raw pointers and read each tensor
     densely at the shape the call implies, so a tensor of another shape, strided, on the
     host or of another type would be read out of bounds or misread."""
-    if (t.__class__ is torch.Tensor and t.is_cuda and t.shape == shape and t.is_contiguous()
-            and dtype in (None, t.dtype) and device in (None, t.device)):
-        return  # the usual case, in one step: the checks below only say what is wrong
     if t is None:
         if optional:
             return
@@ -391,33 +388,51 @@ def _switched(device, stream):
         yield
 
 
+_AS_IS = contextlib.nullcontext()
+
+
 def _at(device, stream):
     """The call's device made current for its launch, and its outputs allocated on its stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    elif torch.cuda.current_device() == device.index:
+        return _AS_IS
     return _switched(device, stream)
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
 def _raw_stream(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
 
 
-def _expect_pool(codes, scales):
-    """Codes [n_slots, Hv, dk, dv] and their scales [n_slots, Hv, dk] of an 8-bit pool; returns the
-    format and the pool's sizes."""
+def _ptrs(device, *tensors):
+    """The addresses of a call's tensors, each given as (name, tensor or None, shape, dtype, optional)
+    and checked as _expect does. A decode step of one sequence takes a few microseconds on the
+    GPU: the usual case has to stay short here, and _expect only says what is wrong."""
+    index, out = device.index, []
+    for name, t, shape, dtype, optional in tensors:
+        if t is None and optional:
+            out.append(None)
+            continue
+        try:
+            if t.get_device() == index and t.shape == shape and t.dtype is dtype and t.is_contiguous():
+                out.append(t.data_ptr())
+                continue
+        except AttributeError:
+            pass
+        _expect(name, t, shape, dtype, device)
+        out.append(t.data_ptr())
+    return out
+
+
+def _pool_of(codes):
+    """Format, sizes and device of an 8-bit pool's codes [n_slots, Hv, dk, dv]."""
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() != 4:
         raise ValueError("codes must be a CUDA tensor [n_slots, Hv, dk, dv]")
-    if codes.dtype not in _Q8_FORMAT:
+    fmt = _Q8_FORMAT.get(codes.dtype)
+    if fmt is None:
         raise TypeError(f"codes is {codes.dtype}, expected torch.int8 or torch.float8_e4m3fn")
-    _expect("codes", codes, codes.shape, None, codes.device)
-    _expect("scales", scales, codes.shape[:3], torch.float32, codes.device)
-    return _Q8_FORMAT[codes.dtype], codes.shape
+    return fmt, codes.shape, codes.device
 
 
 def gdn2_state_store(S, codes, scales, slots=None, stream=None):
@@ -426,14 +441,14 @@ def gdn2_state_store(S, codes, scales, slots=None, stream=None):
     S fp32 [N,Hv,dk,dv]; codes int8 or float8_e4m3fn [n_slots,Hv,dk,dv] and scales fp32
     [n_slots,Hv,dk], written at each sequence's slot; slots int32 [N] (out of range: not stored;
     no two sequences may share one) or None (slot n). Returns (codes, scales)."""
-    fmt, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
-    dev = codes.device
+    fmt, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
     n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else 0
-    _expect("S", S, (n, h_v, dk, dv), torch.float32, dev)
-    _expect("slots", slots, (n,), torch.int32, dev, optional=True)
+    S_, slots_, codes_, scales_ = _ptrs(
+        dev, ("S", S, (n, h_v, dk, dv), torch.float32, False), ("slots", slots, (n,), torch.int32, True),
+        ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False))
     with _at(dev, stream):
-        _check(load_library().gdn2_state_store(n, h_v, dk, dv, fmt, S.data_ptr(), _p(slots), codes.data_ptr(),
-                                               scales.data_ptr(), n_slots, _raw_stream(dev, stream)))
+        _check(load_library().gdn2_state_store(n, h_v, dk, dv, fmt, S_, slots_, codes_, scales_, n_slots,
+                                               _raw_stream(dev, stream)))
     return codes, scales
 
 
@@ -441,24 +456,25 @@ def gdn2_state_load(codes, scales, slots=None, n_seq=None, S=None, stream=None):
     """Read states back from an 8-bit pool, for example as the S0 of a prefill: fp32 [N,Hv,dk,dv].
     slots int32 [N] (out of range: the zero state) or None (slot n of the first ``n_seq``, by
     default all, slots). ``S``, if given, is written and returned."""
-    fmt, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
-    dev = codes.device
+    fmt, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
     if slots is not None:
         n = slots.numel() if isinstance(slots, torch.Tensor) else 0
-        _expect("slots", slots, (n,), torch.int32, dev)
     else:
         n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else n_slots
     if n_seq is not None:
-        if slots is not None or S is not None:
-            if int(n_seq) != n:
-                raise ValueError(f"n_seq = {n_seq}, but slots or S has {n} sequences")
+        if (slots is not None or S is not None) and int(n_seq) != n:
+            raise ValueError(f"n_seq = {n_seq}, but slots or S has {n} sequences")
         n = int(n_seq)
-    _expect("S", S, (n, h_v, dk, dv), torch.float32, dev, optional=True)
+    shape = (n, h_v, dk, dv)
+    slots_, S_, codes_, scales_ = _ptrs(
+        dev, ("slots", slots, (n,), torch.int32, True), ("S", S, shape, torch.float32, True),
+        ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False))
     with _at(dev, stream):
         if S is None:
-            S = torch.empty((n, h_v, dk, dv), dtype=torch.float32, device=dev)
-        _check(load_library().gdn2_state_load(n, h_v, dk, dv, fmt, codes.data_ptr(), scales.data_ptr(), n_slots,
-                                              _p(slots), S.data_ptr(), _raw_stream(dev, stream)))
+            S = torch.empty(shape, dtype=torch.float32, device=dev)
+            S_ = S.data_ptr()
+        _check(load_library().gdn2_state_load(n, h_v, dk, dv, fmt, codes_, scales_, n_slots, slots_, S_,
+                                              _raw_stream(dev, stream)))
     return S
 
 
@@ -473,31 +489,41 @@ def gdn2_decode_multi_q8(q, k, v, log_alpha, b, w, codes, scales, slots=None, sl
     (None: where it was read; out of range: nowhere). Returns (o, code_steps [N,n_tok,Hv,dk,dv],
     scale_steps [N,n_tok,Hv,dk]), the last two -- the state after each token -- None unless given
     or wanted."""
-    fmt, (n_slots, p_h, p_dk, p_dv) = _expect_pool(codes, scales)
+    fmt, (n_slots, p_h, p_dk, p_dv), dev = _pool_of(codes)
     if o is not None:
         out_dtype = o.dtype
-    N, n_tok = (v.shape[0], v.shape[1]) if isinstance(v, torch.Tensor) and v.dim() == 4 else (0, 0)
-    h_qk, dk, h_v, dv, dev = _expect_tokens(q, k, v, log_alpha, b, w, (N, n_tok), prologue)
-    _expect("codes", codes, (n_slots, h_v, dk, dv), None, dev)
-    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
-    _expect("slots_out", slots_out, (N,), torch.int32, dev, optional=True)
-    _expect("o", o, (N, n_tok, h_v, dv), None, dev, optional=True)
-    _expect("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, dev, optional=True)
-    _expect("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, dev, optional=True)
+    for name, t in (("q", q), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (N, n_tok) + (heads, channels)")
+    N, n_tok, h_v, dv = v.shape
+    _, _, h_qk, dk = q.shape
+    dt, f32, i32 = q.dtype, torch.float32, torch.int32
+    sk, sv = (N, n_tok, h_v, dk), (N, n_tok, h_v, dv)
+    shape = Shape(N, N * n_tok, h_qk, h_v, dk, dv, _dtype_code(dt), _dtype_code(out_dtype))
+    q_, k_, v_, la_, b_, w_, codes_, scales_, slots_, out_, o_, cs_, ss_ = _ptrs(
+        dev, ("q", q, (N, n_tok, h_qk, dk), dt, False), ("k", k, (N, n_tok, h_qk, dk), dt, False),
+        ("v", v, sv, dt, False), ("log_alpha", log_alpha, sk, dt if prologue else f32, False),
+        ("b", b, sk, dt, False), ("w", w, sv, dt, False),
+        ("codes", codes, (n_slots, h_v, dk, dv), codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), f32, False),
+        ("slots", slots, (N,), i32, True), ("slots_out", slots_out, (N,), i32, True), ("o", o, sv, out_dtype, True),
+        ("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, True),
+        ("scale_steps", scale_steps, sk, f32, True))
     if (code_steps is None) != (scale_steps is None):
         raise ValueError("code_steps and scale_steps are given together or not at all")
-    shape = Shape(N, N * n_tok, h_qk, h_v, dk, dv, _dtype_code(v.dtype), _dtype_code(out_dtype))
     with _at(dev, stream):
         if o is None:
-            o = torch.empty((N, n_tok, h_v, dv), dtype=out_dtype, device=dev)
+            o = torch.empty(sv, dtype=out_dtype, device=dev)
+            o_ = o.data_ptr()
         if code_steps is None and want_steps:
             code_steps = torch.empty((N, n_tok, h_v, dk, dv), dtype=codes.dtype, device=dev)
-            scale_steps = torch.empty((N, n_tok, h_v, dk), dtype=torch.float32, device=dev)
+            scale_steps = torch.empty(sk, dtype=f32, device=dev)
+            cs_, ss_ = code_steps.data_ptr(), scale_steps.data_ptr()
         lib = load_library()
         fn = lib.gdn2_decode_multi_q8_prologue if prologue else lib.gdn2_decode_multi_q8
-        _check(fn(ctypes.byref(shape), fmt, n_tok, _p(slots), _p(slots_out), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                  log_alpha.data_ptr(), b.data_ptr(), w.data_ptr(), codes.data_ptr(), scales.data_ptr(), n_slots,
-                  o.data_ptr(), _p(code_steps), _p(scale_steps), _raw_stream(dev, stream)))
+        _check(fn(ctypes.byref(shape), fmt, n_tok, slots_, out_, q_, k_, v_, la_, b_, w_, codes_, scales_, n_slots, o_,
+                  cs_, ss_, _raw_stream(dev, stream)))
     return o, code_steps, scale_steps
 
 
@@ -513,28 +539,25 @@ def gdn2_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_samp
     if not isinstance(target_probs, torch.Tensor) or not target_probs.is_cuda or target_probs.dim() != 3:
         raise ValueError("target_probs must be a CUDA tensor [N, n_draft + 1, V]")
     N, n1, V = target_probs.shape
-    dt, dev = target_probs.dtype, target_probs.device
+    dt, dev, f32, i32 = target_probs.dtype, target_probs.device, torch.float32, torch.int32
     code = _dtype_code(dt)
     n = n1 - 1
     if n < 0:
         raise ValueError("target_probs has no place for a token: its second size is n_draft + 1")
-    _expect("target_probs", target_probs, (N, n1, V), dt, dev)
-    _expect("draft_probs", draft_probs, (N, n, V), dt, dev, optional=True)
-    _expect("draft_tokens", draft_tokens, (N, n), torch.int32, dev)
-    _expect("u_accept", u_accept, (N, n), torch.float32, dev)
-    _expect("u_sample", u_sample, (N,), torch.float32, dev)
-    _expect("n_drafted", n_drafted, (N,), torch.int32, dev, optional=True)
-    _expect("n_accepted", n_accepted, (N,), torch.int32, dev, optional=True)
-    _expect("tokens", tokens, (N, n1), torch.int32, dev, optional=True)
+    p_, q_, d_, u_, ul_, n_, acc_, tok_ = _ptrs(
+        dev, ("target_probs", target_probs, (N, n1, V), dt, False), ("draft_probs", draft_probs, (N, n, V), dt, True),
+        ("draft_tokens", draft_tokens, (N, n), i32, False), ("u_accept", u_accept, (N, n), f32, False),
+        ("u_sample", u_sample, (N,), f32, False), ("n_drafted", n_drafted, (N,), i32, True),
+        ("n_accepted", n_accepted, (N,), i32, True), ("tokens", tokens, (N, n1), i32, True))
     with _at(dev, stream):
         if n_accepted is None:
-            n_accepted = torch.empty((N,), dtype=torch.int32, device=dev)
+            n_accepted = torch.empty((N,), dtype=i32, device=dev)
+            acc_ = n_accepted.data_ptr()
         if tokens is None:
-            tokens = torch.empty((N, n1), dtype=torch.int32, device=dev)
-        _check(load_library().gdn2_verify_drafts(
-            N, n, V, code, target_probs.data_ptr(), _p(draft_probs), draft_tokens.data_ptr(), _p(n_drafted),
-            u_accept.data_ptr(), u_sample.data_ptr(), n_accepted.data_ptr(), tokens.data_ptr(),
-            _raw_stream(dev, stream)))
+            tokens = torch.empty((N, n1), dtype=i32, device=dev)
+            tok_ = tokens.data_ptr()
+        _check(load_library().gdn2_verify_drafts(N, n, V, code, p_, q_, d_, n_, u_, ul_, acc_, tok_,
+                                                 _raw_stream(dev, stream)))
     return n_accepted, tokens
 
 
@@ -548,30 +571,29 @@ def gdn2_state_commit(S_steps, index, S_pool, slots=None, stream=None):
     n_slots, h_v, dk, dv = S_pool.shape
     dev = S_pool.device
     N, n_tok = S_steps.shape[:2] if isinstance(S_steps, torch.Tensor) and S_steps.dim() == 5 else (0, 0)
-    _expect("S_pool", S_pool, (n_slots, h_v, dk, dv), torch.float32, dev)
-    _expect("S_steps", S_steps, (N, n_tok, h_v, dk, dv), torch.float32, dev)
-    _expect("index", index, (N,), torch.int32, dev)
-    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
+    pool_, steps_, index_, slots_ = _ptrs(
+        dev, ("S_pool", S_pool, (n_slots, h_v, dk, dv), torch.float32, False),
+        ("S_steps", S_steps, (N, n_tok, h_v, dk, dv), torch.float32, False), ("index", index, (N,), torch.int32, False),
+        ("slots", slots, (N,), torch.int32, True))
     with _at(dev, stream):
-        _check(load_library().gdn2_state_commit(N, h_v, dk, dv, n_tok, S_steps.data_ptr(), index.data_ptr(), _p(slots),
-                                                S_pool.data_ptr(), n_slots, _raw_stream(dev, stream)))
+        _check(load_library().gdn2_state_commit(N, h_v, dk, dv, n_tok, steps_, index_, slots_, pool_, n_slots,
+                                                _raw_stream(dev, stream)))
     return S_pool
 
 
 def gdn2_state_commit_q8(code_steps, scale_steps, index, codes, scales, slots=None, stream=None):
     """gdn2_state_commit in an 8-bit pool: code_steps [N,n_tok,Hv,dk,dv] and scale_steps
     [N,n_tok,Hv,dk] of gdn2_decode_multi_q8 into codes and scales. Returns (codes, scales)."""
-    _, (n_slots, h_v, dk, dv) = _expect_pool(codes, scales)
-    dev = codes.device
+    _, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
     N, n_tok = code_steps.shape[:2] if isinstance(code_steps, torch.Tensor) and code_steps.dim() == 5 else (0, 0)
-    _expect("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, dev)
-    _expect("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, dev)
-    _expect("index", index, (N,), torch.int32, dev)
-    _expect("slots", slots, (N,), torch.int32, dev, optional=True)
+    codes_, scales_, cs_, ss_, index_, slots_ = _ptrs(
+        dev, ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False),
+        ("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, False),
+        ("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, False), ("index", index, (N,), torch.int32, False),
+        ("slots", slots, (N,), torch.int32, True))
     with _at(dev, stream):
-        _check(load_library().gdn2_state_commit_q8(
-            N, h_v, dk, dv, n_tok, code_steps.data_ptr(), scale_steps.data_ptr(), index.data_ptr(), _p(slots),
-            codes.data_ptr(), scales.data_ptr(), n_slots, _raw_stream(dev, stream)))
+        _check(load_library().gdn2_state_commit_q8(N, h_v, dk, dv, n_tok, cs_, ss_, index_, slots_, codes_, scales_,
+                                                   n_slots, _raw_stream(dev, stream)))
     return codes, scales
 
 

@@ -17,6 +17,9 @@
 // column sums cross the warps through shared memory, which is the one barrier per token. The
 // arithmetic runs on pairs of rows: packed two-wide instructions take the rows' factors as they
 // lie in shared memory.
+#include <algorithm>
+#include <atomic>
+
 #include "q8.cuh"
 #include "tc_ptx.cuh"
 
@@ -417,21 +420,34 @@ template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
 cudaError_t launch(const Params& p, const Q8Args& a, cudaStream_t st) {
     using C = Cfg<DK, DV, kFmt, T, kPro, kOne>;
     auto kern = decode_q8_kernel<DK, DV, kFmt, T, kPro, kOne>;
-    Ring ring{0, (C::TOK + p.n_tok * C::REC + 127) & ~127,
-              {a.codes, a.scales, p.k, p.q, p.b, kPro ? p.a_raw : static_cast<const void*>(p.log_alpha), p.v, p.w}};
+    const auto stage_bytes = [](int n_tok) { return (C::TOK + n_tok * C::REC + 127) & ~127; };
     // three stages (two items ahead) where the SM's CTAs have room for them, else two
-    ring.stages = C::CTAS * (3 * ring.stage_bytes + 22 * 1024) <= 224 * 1024 ? 3 : 2;
+    const auto stages = [&](int n_tok) { return C::CTAS * (3 * stage_bytes(n_tok) + 22 * 1024) <= 224 * 1024 ? 3 : 2; };
+    const Ring ring{stages(p.n_tok), stage_bytes(p.n_tok),
+                    {a.codes, a.scales, p.k, p.q, p.b, kPro ? p.a_raw : static_cast<const void*>(p.log_alpha), p.v, p.w}};
     const int smem = ring.stages * ring.stage_bytes;
-    int dev = 0, sms = 0, per_sm = 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::NT, smem);
+    // CTAs that the device holds, looked up once per device and token count: for a small batch these
+    // queries take as long as the launch
+    constexpr int kDevices = 16;
+    static std::atomic<int> resident[kDevices][GDN2_DECODE_MAX_TOKENS + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    int ctas = dev < kDevices ? resident[dev][p.n_tok].load(std::memory_order_relaxed) : 0;
+    if (ctas == 0) {
+        int sms = 0, per_sm = 0, most = 0;
+        for (int t = 1; t <= (kOne ? 1 : GDN2_DECODE_MAX_TOKENS); ++t) most = std::max(most, stages(t) * stage_bytes(t));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::NT, smem);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        ctas = sms * per_sm;
+        if (dev < kDevices) resident[dev][p.n_tok].store(ctas, std::memory_order_relaxed);
+    }
     const int items = p.n_seq * p.h_v;
-    kern<<<items < sms * per_sm ? items : sms * per_sm, C::NT, smem, st>>>(p, a, ring);
+    kern<<<std::min(items, ctas), C::NT, smem, st>>>(p, a, ring);
     return cudaGetLastError();
 }
 
