@@ -120,8 +120,9 @@ def test_fused_preprocessing(g, oracle_mod, fmt, dtype, n_tok, dk, dv):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dv", [64, 128])
-def test_bf16_output_is_the_fp32_one_rounded(g, fmt, dv):
-    d = _tokens(3, 2, 2, 2, 64, dv, torch.bfloat16, seed=10)
+@pytest.mark.parametrize("n_tok", [1, 2])
+def test_bf16_output_is_the_fp32_one_rounded(g, fmt, dv, n_tok):
+    d = _tokens(3, n_tok, 2, 2, 64, dv, torch.bfloat16, seed=10)
     codes, scales = _pool(3, 2, 64, dv, fmt, seed=10)
     c2, s2 = codes.clone(), scales.clone()
     o32, _, _ = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales)
@@ -131,9 +132,10 @@ def test_bf16_output_is_the_fp32_one_rounded(g, fmt, dv):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_states_written_elsewhere(g, fmt):
+@pytest.mark.parametrize("n_tok", [1, 2])
+def test_states_written_elsewhere(g, fmt, n_tok):
     """Two sequences go on from one prefix's slot, each in a slot of its own; one writes nowhere."""
-    d = _tokens(4, 2, 2, 2, 128, 128, torch.bfloat16, seed=11)
+    d = _tokens(4, n_tok, 2, 2, 128, 128, torch.bfloat16, seed=11)
     codes, scales = _pool(8, 2, 128, 128, fmt, seed=11)
     c0, s0 = codes.clone(), scales.clone()
     slots, out = [5, 5, 6, 7], [0, 1, -1, 7]
@@ -150,16 +152,18 @@ def test_states_written_elsewhere(g, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_more_items_than_the_gpu_holds(g, fmt):
+@pytest.mark.parametrize("n_tok", [1, 2])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64), (128, 128)])
+def test_more_items_than_the_gpu_holds(g, fmt, n_tok, dk, dv):
     """Enough (sequence, head) pairs that a resident CTA takes several: bit for bit what one sequence
     at a time gives, with skipped sequences among them."""
-    N, H, n_tok = 160, 32, 2
-    d = _tokens(N, n_tok, H, H, 64, 128, torch.bfloat16, seed=12)
-    codes, scales = _pool(N, H, 64, 128, fmt, seed=12)
+    N, H = 160, 32
+    d = _tokens(N, n_tok, H, H, dk, dv, torch.bfloat16, seed=12)
+    codes, scales = _pool(N, H, dk, dv, fmt, seed=12)
     c0, s0 = codes.clone(), scales.clone()
     slots = torch.randperm(N, generator=torch.Generator().manual_seed(2)).to(torch.int32)
     slots[::7] = -1
-    o = torch.full((N, n_tok, H, 128), 123.0, device="cuda")
+    o = torch.full((N, n_tok, H, dv), 123.0, device="cuda")
     g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, slots=slots.cuda(), o=o)
     for n in (1, 2, 50, 97, 158, 159):
         s = int(slots[n])
@@ -173,7 +177,8 @@ def test_more_items_than_the_gpu_holds(g, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_special_states_and_decays(g, fmt):
+@pytest.mark.parametrize("steps", [False, True])
+def test_special_states_and_decays(g, fmt, steps):
     """A zero state, a row read back as NaN, a decay that erases everything (log_alpha = -inf) and
     infinite tokens: what is finite stays exact, what is not shows in the output and in the pool."""
     d = _tokens(5, 1, 1, 1, 64, 64, torch.float32, seed=13)
@@ -187,7 +192,7 @@ def test_special_states_and_decays(g, fmt):
     d["log_alpha"][3] = 0.0  # no decay, no edit: the state stays
     d["v"][4, 0, 0, 5] = float("inf")
     before = R.read_back(codes, scales)
-    o, _, _ = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales)
+    o, _, _ = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, want_steps=steps)
     torch.cuda.synchronize()
     f = {k_: t[:, 0, 0].double().cpu().numpy() for k_, t in d.items()}
     x = f["w"] * f["v"]
@@ -279,3 +284,26 @@ def test_loads_that_never_land_are_reported(g, n_tok):
     assert torch.all(o == 123.0) and torch.equal(codes, c0) and torch.equal(scales, s0)
     g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, o=o)
     assert g.gdn2_device_status() == 0 and not torch.any(o == 123.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("steps", [False, True])
+@pytest.mark.parametrize("size", [1e-25, 1e-3, 1e20])
+def test_states_and_keys_of_any_size(g, oracle_mod, fmt, steps, size):
+    """States, keys and queries far from 1, rows of very different size next to each other, and a head whose
+    keys are zero."""
+    d = _tokens(3, 1, 1, 1, 128, 64, torch.float32, seed=18)
+    gen = torch.Generator().manual_seed(18)
+    S = torch.randn(3, 1, 128, 64, generator=gen) * size * torch.exp(4 * torch.randn(3, 1, 128, 1, generator=gen))
+    d["k"][1] *= 1e-12
+    d["q"][1] *= 1e9
+    d["k"][2] = 0.0
+    d["v"] *= size
+    c, sc = R.quantise(S.numpy(), fmt)
+    codes, scales = torch.from_numpy(c.astype(np.float32)).cuda().to(fmt), torch.from_numpy(sc).cuda()
+    S0 = R.read_back(codes, scales)
+    o, _, _ = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, want_steps=steps)
+    for n in range(3):
+        ref_o, ref_s = _oracle(oracle_mod, d, n, 1, torch.from_numpy(S0[n]))
+        assert rel_err(o[n], ref_o) <= TOL32
+        _check_written(codes[n], scales[n], ref_s, fmt)
