@@ -116,7 +116,7 @@ extern "C" {
 
 const char* gdn2_last_error_string(void) { return g_err; }
 
-int gdn2_version(void) { return 200; }
+int gdn2_version(void) { return 210; }
 
 gdn2_status gdn2_device_status(unsigned int* flags, gdn2_stream_t stream) {
     if (!flags) return fail(GDN2_ERR_INVALID_ARG, "flags is NULL");

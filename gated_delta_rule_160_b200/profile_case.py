@@ -6,6 +6,9 @@
     python -m gated_delta_rule_160_b200.profile_case --kernel bwd --n-seq 2 --T 1024 --iters 2
     python -m gated_delta_rule_160_b200.profile_case --kernel grouped --n-seq 2 --T 8192 --iters 3
     python -m gated_delta_rule_160_b200.profile_case --kernel serving --n-seq 64 --iters 3
+    python -m gated_delta_rule_160_b200.profile_case --kernel q8 --n-seq 128 --iters 3
+    python -m gated_delta_rule_160_b200.profile_case --kernel q8_drafts --n-seq 64 --iters 3
+    python -m gated_delta_rule_160_b200.profile_case --kernel verify --n-seq 128 --iters 3
 
 ``chunk`` runs gdn2_chunk_fwd on the first ``n-seq`` sequences of the 16-head, T=4096,
 d=128 bf16 prefill workload (2 sequences: 268 MB of inputs, larger than L2; ``T`` cuts them);
@@ -16,7 +19,10 @@ gdn2_chunk_bwd (gradients of sum(o * dO)) on the prefill workload's first ``n-se
 sequences; ``grouped`` runs gdn2_chunk_fwd on the grouped-head workload (16 query/key heads
 shared by 32 value heads, with an initial state), its sequences cut to ``T`` tokens;
 ``serving`` runs gdn2_decode_multi (4 tokens per sequence) on ``n-seq`` sequences of the
-32-head decode workload whose states sit at seeded-random slots of a pool twice as large. Each
+32-head decode workload whose states sit at seeded-random slots of a pool twice as large; ``q8``
+runs gdn2_decode_multi_q8 (e4m3 codes, one token) on ``n-seq`` sequences of that workload, and
+``q8_drafts`` the same with 4 tokens and the state after each; ``verify`` runs gdn2_verify_drafts on
+``n-seq`` sequences of 4 drafts over 131072 tokens. Each
 kernel is launched ``iters`` times; profile the last launches (ncu -s / -c).
 """
 import argparse
@@ -29,7 +35,8 @@ from gated_delta_rule_160_b200 import workloads as W
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--kernel", choices=["chunk", "prologue", "decode", "bwd", "grouped", "serving"], default="chunk")
+    ap.add_argument("--kernel", choices=["chunk", "prologue", "decode", "bwd", "grouped", "serving", "q8", "q8_drafts", "verify"],
+                    default="chunk")
     ap.add_argument("--n-seq", type=int, default=2)
     ap.add_argument("--T", type=int, default=None, help="tokens per sequence (chunk, bwd, grouped)")
     ap.add_argument("--iters", type=int, default=3)
@@ -81,6 +88,29 @@ def main():
         o = torch.empty((N, n_tok, wl.h_v, wl.dv), dtype=torch.float32, device="cuda")
         for _ in range(a.iters):
             G.gdn2_decode_multi(*(x[k] for k in ("q", "k", "v", "log_alpha", "b", "w")), pool, slots=slots, o=o)
+    elif a.kernel in ("q8", "q8_drafts"):
+        wl = W.WORKLOADS["decode_256seq_h32"]
+        N, n_tok = a.n_seq, 4 if a.kernel == "q8_drafts" else 1
+        codes = torch.zeros((N, wl.h_v, wl.dk, wl.dv), dtype=torch.float8_e4m3fn, device="cuda")
+        scales = torch.zeros((N, wl.h_v, wl.dk), dtype=torch.float32, device="cuda")
+        G.gdn2_state_store(W.decode_state(wl, "cuda", n_seq=N), codes, scales)
+        t_ = W.token_inputs(N * n_tok, wl.h_qk, wl.h_v, wl.dk, wl.dv, wl.dtype, "cuda", wl.seed * 7919)
+        x = {k: t.view(N, n_tok, *t.shape[1:]) for k, t in t_.items()}
+        steps = {}
+        if a.kernel == "q8_drafts":
+            steps = dict(code_steps=torch.zeros((N, n_tok) + codes.shape[1:], dtype=codes.dtype, device="cuda"),
+                         scale_steps=torch.zeros((N, n_tok) + scales.shape[1:], device="cuda"))
+        for _ in range(a.iters):
+            G.gdn2_decode_multi_q8(*(x[k] for k in ("q", "k", "v", "log_alpha", "b", "w")), codes, scales, **steps)
+    elif a.kernel == "verify":
+        N, n, V = a.n_seq, 4, 131072
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        logits = 3 * torch.randn(N, n + 1, V, generator=gen, device="cuda")
+        near = 0.9 * logits[:, :n] + torch.randn(N, n, V, generator=gen, device="cuda")
+        args = (torch.softmax(logits, -1), torch.softmax(near, -1), near.argmax(-1).to(torch.int32),
+                torch.rand(N, n, generator=gen, device="cuda"), torch.rand(N, generator=gen, device="cuda"))
+        for _ in range(a.iters):
+            G.gdn2_verify_drafts(*args)
     else:
         wl = W.WORKLOADS["decode_256seq_h32"]
         S = W.decode_state(wl, "cuda", n_seq=a.n_seq)
