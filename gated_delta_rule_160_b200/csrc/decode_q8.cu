@@ -17,6 +17,12 @@
 // column sums cross the warps through shared memory, which is the one barrier per token. The
 // arithmetic runs on pairs of rows: packed two-wide instructions take the rows' factors as they
 // lie in shared memory.
+//
+// Measured on B200, 256 sequences x 32 heads x 128 x 128, e4m3, one token: 83.0 us for 0.296 GB of
+// codes, scales and tokens (3.56 TB/s, 0.55 of the copy bandwidth; the fp32 pool takes 165 us). Not
+// HBM bounds it but the 6.1 K warp instructions of an item: unpacking, two sums, the update, the
+// magnitudes, rounding; 55 % of issue slots, fp32 pipe 41 %. 64 sequences, 4 tokens with the state
+// after each: 86.2 us.
 #include <algorithm>
 #include <atomic>
 
@@ -89,7 +95,8 @@ struct Ring {
 
 // kOne: one token and no per-token states. 4 CTAs of 4 warps then fit an SM, and the work that a
 // warp does once per token is spread over twice the rows: a thread keeps the values of one half of its
-// rows from the sums to the update, and reads the other half's codes again. Otherwise 2 CTAs of 8
+// rows from the sums to the update, and reads the other half's codes again (85.5 us with 4 CTAs of
+// 4 warps that read all of them again, 101.6 us with 2 of 8 that keep all). Otherwise 2 CTAs of 8
 // warps, the state in registers from token to token.
 template <int DK, int DV, int kFmt, typename T, bool kPro, bool kOne>
 struct Cfg {

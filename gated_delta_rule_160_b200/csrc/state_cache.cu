@@ -3,7 +3,9 @@
 // the state after the last accepted token put back (gdn2_state_commit, gdn2_state_commit_q8).
 //
 // All of these are bound by HBM: 5 bytes a state element for store and load, twice the state's
-// own bytes for commit; nothing is read twice.
+// own bytes for commit; nothing is read twice. Measured on B200: 256 x 32 states of 128 x 128
+// stored and loaded in 209 us (1.35 GB, 6.46 TB/s), 185 x 32 fp32 states committed in 120 us
+// (0.78 GB, 6.46 TB/s).
 #include "q8.cuh"
 
 namespace gdn2 {
@@ -14,8 +16,9 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------- store, load
 // One CTA per (sequence, value head). A thread holds four neighbouring columns (a float4, four
 // codes) of DK / RG key rows, so a warp's access covers whole rows: 512 bytes of state, 128 of
-// codes. All loads are issued before the first use. The row's largest magnitude is taken over the
-// 16 or 32 lanes that share the row.
+// codes. All loads are issued before the first use, so a CTA has 64 KB (store) in flight. The row's
+// largest magnitude is taken over the 16 or 32 lanes that share the row: shuffles and quotients are
+// repeated in each of them, which the memory time hides.
 template <int DK, int DV, int kFmt>
 __global__ void __launch_bounds__(kThreads) state_store_kernel(const float* __restrict__ S, const int32_t* __restrict__ slots,
                                                                uint32_t* __restrict__ codes, float* __restrict__ scales,

@@ -6,14 +6,18 @@
 // where r is empty); with all accepted one more token comes from p_m. Tokens are drawn by inverse
 // CDF: the lowest j with r_0 + .. + r_j > u (r_0 + .. + r_{V-1}).
 //
-// Everything is computed in fp64 from the exact values of the inputs: u q is exact (24 + 24 bits), and a
-// sum's rounding, ~1e-16, all but never crosses a border of the CDF, so the order of the sums does not show
-// in the tokens.
+// Acceptance is decided in fp64 from the exact values of the inputs (u q is exact there: 24 + 24 bits).
+// Sums are good to 2^-48 relative, so over 131072 tokens the order of the additions shows in about one
+// draw of 10^9: differences p - q are rounded to fp32 and added in fp64, what the rounding took off is
+// exact in fp32 and added apart. (Both operands converted to fp64 cost 61 us where this takes 49.)
 //
-// The work is one row of p and one of q a sequence, so a cluster of up to 8 CTAs shares a sequence: each warp
-// sums segments of 1024 weights (all 16-byte loads of a segment in flight at once), the CTAs exchange
-// their sums through distributed shared memory, and the CTA that holds the border scans its
-// segment sums and then that one segment again, out of L2. No workspace, no atomics on memory, one launch.
+// The work is one row of p and one of q a sequence: HBM. A cluster of up to 8 CTAs shares a sequence: each
+// warp sums segments of 1024 weights with half a segment in flight, the CTAs exchange their sums
+// through distributed shared memory, and the CTA that holds the border scans its segment sums and then that
+// one segment again, out of L2. No workspace, no atomics on memory, one launch. Measured on B200: 256
+// sequences, 4 drafts, 131072 fp32 values a row: 49.4 us, 0.84 of what the rows take at the copy
+// bandwidth; one sequence, 3 drafts, 32768 values: 6.8 us, the latency of drafts, their
+// probabilities, the row and its segment again, one after the other.
 #include <cooperative_groups.h>
 
 #include <algorithm>
