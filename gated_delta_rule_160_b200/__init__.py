@@ -1,9 +1,9 @@
 """libgdn2: the Gated DeltaNet-2 state recurrence on B200 (sm_100a).
 
-This package is a thin ctypes binding over the C ABI declared in ``include/gdn2.h``; every
-step of the recurrence runs in the CUDA kernels of ``libgdn2.so``. PyTorch provides device
-memory and streams only. There is no CPU fallback: if the library is missing or fails to
-load, importing the functions below raises.
+This package is a thin binding over the C ABI declared in ``include/gdn2.h``, by ctypes and, for
+the operators around the state pool, by ``csrc/binding.cpp``; every step of the recurrence runs
+in the CUDA kernels of ``libgdn2.so``. PyTorch provides device memory and streams only. There is
+no CPU fallback: if a library is missing or fails to load, the functions below raise.
 
     gdn2_chunk_fwd(q, k, v, log_alpha, b, w, S0=None, cu_seqlens=None, ...) -> (o, S_T)
         (prologue=True: raw projections in, the pre-processing fused)
@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 
 import torch
@@ -65,12 +66,12 @@ class Shape(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("o_dtype", ctypes.c_int)]
 
 
-_lib = None
+_lib = _binding = None
 
 
 def load_library(path: str = LIB_PATH):
     """Load libgdn2.so (built by ``python -m gated_delta_rule_160_b200.build``)."""
-    global _lib
+    global _lib, _binding
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -114,7 +115,14 @@ def load_library(path: str = LIB_PATH):
     lib.gdn2_last_error_string.restype = ctypes.c_char_p
     lib.gdn2_last_error_string.argtypes = []
     lib.gdn2_version.restype = ctypes.c_int
-    _lib = lib
+    try:
+        binding = importlib.import_module("._binding", __name__)
+    except ImportError as e:
+        raise ImportError(f"{e}; run `python -m gated_delta_rule_160_b200.build`") from e
+    binding.init(Gdn2Error, *(ctypes.cast(getattr(lib, name), vp).value for name in (
+        "gdn2_state_store", "gdn2_state_load", "gdn2_decode_multi_q8", "gdn2_decode_multi_q8_prologue",
+        "gdn2_verify_drafts", "gdn2_state_commit", "gdn2_state_commit_q8", "gdn2_last_error_string")))
+    _lib, _binding = lib, binding
     return lib
 
 
@@ -379,60 +387,12 @@ def gdn2_chunk(q, k, v, log_alpha, b, w, S0=None, cu_seqlens=None, n_seq=None):
 
 # ---------------------------------------------------------------- around the state pool
 
-_Q8_FORMAT = {torch.int8: GDN2_Q8_INT8, torch.float8_e4m3fn: GDN2_Q8_E4M3}
-
-
-@contextlib.contextmanager
-def _switched(device, stream):
-    with torch.cuda.device(device), _on(stream):
-        yield
-
-
-_AS_IS = contextlib.nullcontext()
-
-
-def _at(device, stream):
-    """The call's device made current for its launch, and its outputs allocated on its stream."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    elif torch.cuda.current_device() == device.index:
-        return _AS_IS
-    return _switched(device, stream)
-
-
-def _raw_stream(device, stream):
-    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
-
-
-def _ptrs(device, *tensors):
-    """The addresses of a call's tensors, each given as (name, tensor or None, shape, dtype, optional)
-    and checked as _expect does. A decode step of one sequence takes a few microseconds on the
-    GPU: the usual case has to stay short here, and _expect only says what is wrong."""
-    index, out = device.index, []
-    for name, t, shape, dtype, optional in tensors:
-        if t is None and optional:
-            out.append(None)
-            continue
-        try:
-            if t.get_device() == index and t.shape == shape and t.dtype is dtype and t.is_contiguous():
-                out.append(t.data_ptr())
-                continue
-        except AttributeError:
-            pass
-        _expect(name, t, shape, dtype, device)
-        out.append(t.data_ptr())
-    return out
-
-
-def _pool_of(codes):
-    """Format, sizes and device of an 8-bit pool's codes [n_slots, Hv, dk, dv]."""
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() != 4:
-        raise ValueError("codes must be a CUDA tensor [n_slots, Hv, dk, dv]")
-    fmt = _Q8_FORMAT.get(codes.dtype)
-    if fmt is None:
-        raise TypeError(f"codes is {codes.dtype}, expected torch.int8 or torch.float8_e4m3fn")
-    return fmt, codes.shape, codes.device
+def _bound():
+    """The binding of these operators (csrc/binding.cpp): it checks every tensor as _expect does, makes their
+    device current, allocates missing outputs on the call's stream and calls the library."""
+    if _binding is None:
+        load_library()
+    return _binding
 
 
 def gdn2_state_store(S, codes, scales, slots=None, stream=None):
@@ -441,41 +401,14 @@ def gdn2_state_store(S, codes, scales, slots=None, stream=None):
     S fp32 [N,Hv,dk,dv]; codes int8 or float8_e4m3fn [n_slots,Hv,dk,dv] and scales fp32
     [n_slots,Hv,dk], written at each sequence's slot; slots int32 [N] (out of range: not stored;
     no two sequences may share one) or None (slot n). Returns (codes, scales)."""
-    fmt, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
-    n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else 0
-    S_, slots_, codes_, scales_ = _ptrs(
-        dev, ("S", S, (n, h_v, dk, dv), torch.float32, False), ("slots", slots, (n,), torch.int32, True),
-        ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False))
-    with _at(dev, stream):
-        _check(load_library().gdn2_state_store(n, h_v, dk, dv, fmt, S_, slots_, codes_, scales_, n_slots,
-                                               _raw_stream(dev, stream)))
-    return codes, scales
+    return _bound().store(S, codes, scales, slots, stream)
 
 
 def gdn2_state_load(codes, scales, slots=None, n_seq=None, S=None, stream=None):
     """Read states back from an 8-bit pool, for example as the S0 of a prefill: fp32 [N,Hv,dk,dv].
     slots int32 [N] (out of range: the zero state) or None (slot n of the first ``n_seq``, by
     default all, slots). ``S``, if given, is written and returned."""
-    fmt, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
-    if slots is not None:
-        n = slots.numel() if isinstance(slots, torch.Tensor) else 0
-    else:
-        n = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else n_slots
-    if n_seq is not None:
-        if (slots is not None or S is not None) and int(n_seq) != n:
-            raise ValueError(f"n_seq = {n_seq}, but slots or S has {n} sequences")
-        n = int(n_seq)
-    shape = (n, h_v, dk, dv)
-    slots_, S_, codes_, scales_ = _ptrs(
-        dev, ("slots", slots, (n,), torch.int32, True), ("S", S, shape, torch.float32, True),
-        ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False))
-    with _at(dev, stream):
-        if S is None:
-            S = torch.empty(shape, dtype=torch.float32, device=dev)
-            S_ = S.data_ptr()
-        _check(load_library().gdn2_state_load(n, h_v, dk, dv, fmt, codes_, scales_, n_slots, slots_, S_,
-                                              _raw_stream(dev, stream)))
-    return S
+    return _bound().load(codes, scales, slots, n_seq, S, stream)
 
 
 def gdn2_decode_multi_q8(q, k, v, log_alpha, b, w, codes, scales, slots=None, slots_out=None, o=None,
@@ -489,42 +422,8 @@ def gdn2_decode_multi_q8(q, k, v, log_alpha, b, w, codes, scales, slots=None, sl
     (None: where it was read; out of range: nowhere). Returns (o, code_steps [N,n_tok,Hv,dk,dv],
     scale_steps [N,n_tok,Hv,dk]), the last two -- the state after each token -- None unless given
     or wanted."""
-    fmt, (n_slots, p_h, p_dk, p_dv), dev = _pool_of(codes)
-    if o is not None:
-        out_dtype = o.dtype
-    for name, t in (("q", q), ("v", v)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dim() != 4:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (N, n_tok) + (heads, channels)")
-    N, n_tok, h_v, dv = v.shape
-    _, _, h_qk, dk = q.shape
-    dt, f32, i32 = q.dtype, torch.float32, torch.int32
-    sk, sv = (N, n_tok, h_v, dk), (N, n_tok, h_v, dv)
-    shape = Shape(N, N * n_tok, h_qk, h_v, dk, dv, _dtype_code(dt), _dtype_code(out_dtype))
-    q_, k_, v_, la_, b_, w_, codes_, scales_, slots_, out_, o_, cs_, ss_ = _ptrs(
-        dev, ("q", q, (N, n_tok, h_qk, dk), dt, False), ("k", k, (N, n_tok, h_qk, dk), dt, False),
-        ("v", v, sv, dt, False), ("log_alpha", log_alpha, sk, dt if prologue else f32, False),
-        ("b", b, sk, dt, False), ("w", w, sv, dt, False),
-        ("codes", codes, (n_slots, h_v, dk, dv), codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), f32, False),
-        ("slots", slots, (N,), i32, True), ("slots_out", slots_out, (N,), i32, True), ("o", o, sv, out_dtype, True),
-        ("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, True),
-        ("scale_steps", scale_steps, sk, f32, True))
-    if (code_steps is None) != (scale_steps is None):
-        raise ValueError("code_steps and scale_steps are given together or not at all")
-    with _at(dev, stream):
-        if o is None:
-            o = torch.empty(sv, dtype=out_dtype, device=dev)
-            o_ = o.data_ptr()
-        if code_steps is None and want_steps:
-            code_steps = torch.empty((N, n_tok, h_v, dk, dv), dtype=codes.dtype, device=dev)
-            scale_steps = torch.empty(sk, dtype=f32, device=dev)
-            cs_, ss_ = code_steps.data_ptr(), scale_steps.data_ptr()
-        lib = load_library()
-        fn = lib.gdn2_decode_multi_q8_prologue if prologue else lib.gdn2_decode_multi_q8
-        _check(fn(ctypes.byref(shape), fmt, n_tok, slots_, out_, q_, k_, v_, la_, b_, w_, codes_, scales_, n_slots, o_,
-                  cs_, ss_, _raw_stream(dev, stream)))
-    return o, code_steps, scale_steps
+    return _bound().decode(q, k, v, log_alpha, b, w, codes, scales, slots, slots_out, o, code_steps, scale_steps,
+                           want_steps, stream, _dtype_code(out_dtype if o is None else o.dtype), prologue)
 
 
 def gdn2_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n_drafted=None,
@@ -536,29 +435,8 @@ def gdn2_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_samp
     u_sample fp32 [N], uniform in [0, 1); n_drafted int32 [N] (a sequence's own number of drafts;
     negative = inactive) or None (n_draft each). Returns (n_accepted int32 [N], tokens int32
     [N,n_draft+1]: the accepted tokens, then the one drawn for the next place, then -1)."""
-    if not isinstance(target_probs, torch.Tensor) or not target_probs.is_cuda or target_probs.dim() != 3:
-        raise ValueError("target_probs must be a CUDA tensor [N, n_draft + 1, V]")
-    N, n1, V = target_probs.shape
-    dt, dev, f32, i32 = target_probs.dtype, target_probs.device, torch.float32, torch.int32
-    code = _dtype_code(dt)
-    n = n1 - 1
-    if n < 0:
-        raise ValueError("target_probs has no place for a token: its second size is n_draft + 1")
-    p_, q_, d_, u_, ul_, n_, acc_, tok_ = _ptrs(
-        dev, ("target_probs", target_probs, (N, n1, V), dt, False), ("draft_probs", draft_probs, (N, n, V), dt, True),
-        ("draft_tokens", draft_tokens, (N, n), i32, False), ("u_accept", u_accept, (N, n), f32, False),
-        ("u_sample", u_sample, (N,), f32, False), ("n_drafted", n_drafted, (N,), i32, True),
-        ("n_accepted", n_accepted, (N,), i32, True), ("tokens", tokens, (N, n1), i32, True))
-    with _at(dev, stream):
-        if n_accepted is None:
-            n_accepted = torch.empty_like(u_sample, dtype=i32)  # half the time of torch.empty
-            acc_ = n_accepted.data_ptr()
-        if tokens is None:
-            tokens = torch.empty((N, n1), dtype=i32, device=dev)
-            tok_ = tokens.data_ptr()
-        _check(load_library().gdn2_verify_drafts(N, n, V, code, p_, q_, d_, n_, u_, ul_, acc_, tok_,
-                                                 _raw_stream(dev, stream)))
-    return n_accepted, tokens
+    return _bound().verify(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n_drafted, n_accepted, tokens,
+                           stream)
 
 
 def gdn2_state_commit(S_steps, index, S_pool, slots=None, stream=None):
@@ -566,35 +444,13 @@ def gdn2_state_commit(S_steps, index, S_pool, slots=None, stream=None):
     [N,n_tok,Hv,dk,dv]) back into the sequence's slot of S_pool fp32 [n_slots,Hv,dk,dv]. index
     int32 [N], for example n_accepted of gdn2_verify_drafts (outside 0..n_tok-1: left as it is);
     slots as for gdn2_decode_multi. Returns S_pool."""
-    if not isinstance(S_pool, torch.Tensor) or not S_pool.is_cuda or S_pool.dim() != 4:
-        raise ValueError("S_pool must be a CUDA tensor [n_slots, Hv, dk, dv]")
-    n_slots, h_v, dk, dv = S_pool.shape
-    dev = S_pool.device
-    N, n_tok = S_steps.shape[:2] if isinstance(S_steps, torch.Tensor) and S_steps.dim() == 5 else (0, 0)
-    pool_, steps_, index_, slots_ = _ptrs(
-        dev, ("S_pool", S_pool, (n_slots, h_v, dk, dv), torch.float32, False),
-        ("S_steps", S_steps, (N, n_tok, h_v, dk, dv), torch.float32, False), ("index", index, (N,), torch.int32, False),
-        ("slots", slots, (N,), torch.int32, True))
-    with _at(dev, stream):
-        _check(load_library().gdn2_state_commit(N, h_v, dk, dv, n_tok, steps_, index_, slots_, pool_, n_slots,
-                                                _raw_stream(dev, stream)))
-    return S_pool
+    return _bound().commit(S_steps, index, S_pool, slots, stream)
 
 
 def gdn2_state_commit_q8(code_steps, scale_steps, index, codes, scales, slots=None, stream=None):
     """gdn2_state_commit in an 8-bit pool: code_steps [N,n_tok,Hv,dk,dv] and scale_steps
     [N,n_tok,Hv,dk] of gdn2_decode_multi_q8 into codes and scales. Returns (codes, scales)."""
-    _, (n_slots, h_v, dk, dv), dev = _pool_of(codes)
-    N, n_tok = code_steps.shape[:2] if isinstance(code_steps, torch.Tensor) and code_steps.dim() == 5 else (0, 0)
-    codes_, scales_, cs_, ss_, index_, slots_ = _ptrs(
-        dev, ("codes", codes, codes.shape, codes.dtype, False), ("scales", scales, (n_slots, h_v, dk), torch.float32, False),
-        ("code_steps", code_steps, (N, n_tok, h_v, dk, dv), codes.dtype, False),
-        ("scale_steps", scale_steps, (N, n_tok, h_v, dk), torch.float32, False), ("index", index, (N,), torch.int32, False),
-        ("slots", slots, (N,), torch.int32, True))
-    with _at(dev, stream):
-        _check(load_library().gdn2_state_commit_q8(N, h_v, dk, dv, n_tok, cs_, ss_, index_, slots_, codes_, scales_,
-                                                   n_slots, _raw_stream(dev, stream)))
-    return codes, scales
+    return _bound().commit_q8(code_steps, scale_steps, index, codes, scales, slots, stream)
 
 
 def gdn2_device_status(stream=None) -> int:

@@ -1,7 +1,8 @@
-"""Build libgdn2.so (the sm_100a CUDA library) in-tree with nvcc.
+"""Build libgdn2.so (the sm_100a CUDA library) in-tree with nvcc, and _binding.so (the host-side
+binding of the serving operators, against the installed torch) with g++.
 
-Usage: ``python -m gated_delta_rule_160_b200.build [--force]``. The library is written next
-to this file so that it travels with the source tree.
+Usage: ``python -m gated_delta_rule_160_b200.build [--force]``. Both are written next
+to this file so that they travel with the source tree.
 """
 from __future__ import annotations
 
@@ -13,6 +14,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn2.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC_FLAGS = [
@@ -43,7 +46,32 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """_binding.so: C++ over torch's headers, no CUDA code."""
+    import sysconfig
+
+    import torch
+    deps = [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp"

@@ -205,3 +205,76 @@ def test_streams_of_another_device_are_refused(g):
     S = W.state_input(1, 1, 64, 64, 0.05, "cuda", seed=1)
     with pytest.raises(ValueError, match="stream is on cuda:7"):
         g.gdn2_state_store(S, torch.zeros(1, 1, 64, 64, dtype=torch.int8, device="cuda"), torch.zeros(1, 1, 64, device="cuda"), stream=Elsewhere())
+
+
+def test_calls_keep_no_references(g):
+    import sys
+    S = W.state_input(2, 1, 64, 64, 0.05, "cuda", seed=2)
+    codes, scales = torch.zeros(2, 1, 64, 64, dtype=torch.int8, device="cuda"), torch.zeros(2, 1, 64, device="cuda")
+    d = {k_: t.view(2, 1, *t.shape[1:]) for k_, t in W.token_inputs(2, 1, 1, 64, 64, torch.float32, "cuda", seed=2).items()}
+    p = torch.full((2, 1, 8), 0.125, device="cuda")
+    none = torch.zeros(2, 0, device="cuda")
+    index = torch.zeros(2, dtype=torch.int32, device="cuda")
+    u = torch.rand(2, device="cuda")
+    held = [S, codes, scales, p, none, index, u, *d.values()]
+
+    def once():
+        g.gdn2_state_store(S, codes, scales)
+        g.gdn2_state_load(codes, scales, S=S)
+        g.gdn2_state_load(codes, scales)
+        _, cs, ss = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, want_steps=True)
+        g.gdn2_state_commit_q8(cs, ss, index, codes, scales)
+        g.gdn2_state_commit(S[:, None], index, S)
+        g.gdn2_verify_drafts(p, None, none.to(torch.int32), none, u)
+        with pytest.raises(ValueError):
+            g.gdn2_state_store(S[:, :, :32].contiguous(), codes, scales)
+
+    once()
+    before = [sys.getrefcount(x) for x in held]
+    torch.cuda.synchronize()
+    memory = torch.cuda.memory_allocated()
+    for _ in range(50):
+        once()
+    torch.cuda.synchronize()
+    assert [sys.getrefcount(x) for x in held] == before and torch.cuda.memory_allocated() == memory
+
+
+def test_calls_from_several_threads(g):
+    """Each thread on its own stream, some of their calls refused: results and messages stay with their thread."""
+    import threading
+    results = {}
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        x = _step_inputs(300 + i)
+        pool, steps = _q8_buffers(torch.int8 if i % 2 else torch.float8_e4m3fn)
+        bufs = _buffers()
+        S = W.state_input(N, H, D, D, 0.05, "cuda", seed=300 + i)
+        slots = _slots()
+        torch.cuda.synchronize()
+        g.gdn2_state_store(S, *pool, slots=slots, stream=stream)
+        errors = []
+        for k in range(20):
+            _step_q8(g, x, pool, steps, slots, *bufs, stream=stream)
+            try:
+                g.gdn2_state_load(pool[0][:1 + i], pool[1][:1 + i], n_seq=2 + i, stream=stream)
+            except g.Gdn2Error as e:
+                errors.append(str(e))
+        stream.synchronize()
+        results[i] = (pool, bufs, errors)
+
+    def alone(i):
+        work(i)
+        return results.pop(i)
+
+    want = [alone(i) for i in range(4)]
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        (pool, bufs, errors), (w_pool, w_bufs, w_errors) = results[i], want[i]
+        assert errors == w_errors and len(errors) == 20 and f"n_slots = {1 + i} too small" in errors[0]
+        assert torch.equal(pool[0].view(torch.uint8), w_pool[0].view(torch.uint8)) and torch.equal(pool[1], w_pool[1])
+        assert all(torch.equal(a, b) for a, b in zip(bufs, w_bufs))
