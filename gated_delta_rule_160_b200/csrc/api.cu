@@ -370,6 +370,8 @@ gdn2_status state_cache(bool store, int n_seq, int h_v, int dk, int dv, gdn2_q8_
     gdn2_status st = check_states(n_seq, h_v, dk, dv, slots, n_slots);
     if (st == GDN2_OK) st = check_format(fmt);
     if (st != GDN2_OK) return st;
+    if ((long long)n_seq * h_v > 0x3fffffffLL)  // two CTAs per state
+        return fail(GDN2_ERR_UNSUPPORTED, "n_seq * h_v = %lld states, above 2^30 - 1", (long long)n_seq * h_v);
     const NamedPtr ps[] = {{"S", S, true}, {"codes", codes, true}, {"scales", scales, true}, {"slots", slots, false, 4}};
     st = check_ptrs(ps, (int)(sizeof ps / sizeof ps[0]));
     if (st != GDN2_OK) return st;

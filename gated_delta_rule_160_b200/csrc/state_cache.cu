@@ -4,7 +4,7 @@
 //
 // All of these are bound by HBM: 5 bytes a state element for store and load, twice the state's
 // own bytes for commit; nothing is read twice. Measured on B200: 256 x 32 states of 128 x 128
-// stored and loaded in 209 us (1.35 GB, 6.46 TB/s), 185 x 32 fp32 states committed in 120 us
+// stored and loaded in 206 us (1.35 GB, 6.56 TB/s), 185 x 32 fp32 states committed in 120 us
 // (0.78 GB, 6.46 TB/s).
 #include "q8.cuh"
 
@@ -12,24 +12,27 @@ namespace gdn2 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kParts = 2;  // CTAs per state (store, load)
 
 // ---------------------------------------------------------------- store, load
-// One CTA per (sequence, value head). A thread holds four neighbouring columns (a float4, four
-// codes) of DK / RG key rows, so a warp's access covers whole rows: 512 bytes of state, 128 of
-// codes. All loads are issued before the first use, so a CTA has 64 KB (store) in flight. The row's
+// A CTA per half of a (sequence, value head)'s key rows: 61 x 16 states take 25.2 us stored and loaded, 27.4
+// with a whole state per CTA (fewer, longer waves), 26.5 with a quarter. (The halves are neighbours in
+// the grid: half a grid apart, 256 x 32 states take 215 us instead of 206.) A thread holds four
+// neighbouring columns (a float4, four codes) of its rows, so a warp's access covers whole rows: 512
+// bytes of state, 128 of codes. All loads are issued before the first use. The row's
 // largest magnitude is taken over the 16 or 32 lanes that share the row: shuffles and quotients are
 // repeated in each of them, which the memory time hides.
 template <int DK, int DV, int kFmt>
 __global__ void __launch_bounds__(kThreads) state_store_kernel(const float* __restrict__ S, const int32_t* __restrict__ slots,
                                                                uint32_t* __restrict__ codes, float* __restrict__ scales,
                                                                int n_slots, int h_v) {
-    constexpr int TPR = DV / 4, RG = kThreads / TPR, RPT = DK / RG;
-    const int n = blockIdx.x / h_v, h = blockIdx.x % h_v;
+    constexpr int TPR = DV / 4, RG = kThreads / TPR, ROWS = DK / kParts, RPT = ROWS / RG;
+    const int item = blockIdx.x / kParts, first = blockIdx.x % kParts * ROWS, n = item / h_v, h = item % h_v;
     const int slot = slots ? slots[n] : n;
     if (slot < 0 || slot >= n_slots) return;  // no slot: nothing to keep
     const int cg = threadIdx.x % TPR, rg = threadIdx.x / TPR;
-    const float4* src = reinterpret_cast<const float4*>(S) + (size_t)blockIdx.x * (DK * TPR) + cg;
-    const size_t row0 = ((size_t)slot * h_v + h) * DK;
+    const float4* src = reinterpret_cast<const float4*>(S) + ((size_t)item * DK + first) * TPR + cg;
+    const size_t row0 = ((size_t)slot * h_v + h) * DK + first;
     float4 s[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) s[i] = __ldcs(src + (rg + RG * i) * TPR);
@@ -50,17 +53,17 @@ template <int DK, int DV, int kFmt>
 __global__ void __launch_bounds__(kThreads) state_load_kernel(const uint32_t* __restrict__ codes, const float* __restrict__ scales,
                                                               const int32_t* __restrict__ slots, float* __restrict__ S,
                                                               int n_slots, int h_v) {
-    constexpr int TPR = DV / 4, RG = kThreads / TPR, RPT = DK / RG;
-    const int n = blockIdx.x / h_v, h = blockIdx.x % h_v;
+    constexpr int TPR = DV / 4, RG = kThreads / TPR, ROWS = DK / kParts, RPT = ROWS / RG;
+    const int item = blockIdx.x / kParts, first = blockIdx.x % kParts * ROWS, n = item / h_v, h = item % h_v;
     const int slot = slots ? slots[n] : n;
     const int cg = threadIdx.x % TPR, rg = threadIdx.x / TPR;
-    float4* dst = reinterpret_cast<float4*>(S) + (size_t)blockIdx.x * (DK * TPR) + cg;
+    float4* dst = reinterpret_cast<float4*>(S) + ((size_t)item * DK + first) * TPR + cg;
     if (slot < 0 || slot >= n_slots) {  // nothing kept: the sequence starts from the zero state
 #pragma unroll
         for (int i = 0; i < RPT; ++i) __stcs(dst + (rg + RG * i) * TPR, make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
-    const size_t row0 = ((size_t)slot * h_v + h) * DK;
+    const size_t row0 = ((size_t)slot * h_v + h) * DK + first;
     uint32_t c[RPT];
     float sc[RPT];
 #pragma unroll
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) state_commit_kernel(const char* __re
 
 template <int DK, int DV, int kFmt>
 cudaError_t launch_cache_t(bool store, const StateCacheArgs& a, cudaStream_t st) {
-    const int grid = a.n_seq * a.h_v;
+    const int grid = kParts * a.n_seq * a.h_v;
     if (store)
         state_store_kernel<DK, DV, kFmt><<<grid, kThreads, 0, st>>>(a.S, a.slots, static_cast<uint32_t*>(a.codes), a.scales, a.n_slots, a.h_v);
     else

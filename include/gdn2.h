@@ -252,7 +252,7 @@ typedef enum { GDN2_Q8_INT8 = 0, GDN2_Q8_E4M3 = 1 } gdn2_q8_format;
  * Quantise n_seq states S [n_seq, h_v, dk, dv] float32 into their slots of the pool (slots: device
  * int32 [n_seq]; NULL means slot n, and then n_slots must be at least n_seq). A sequence whose
  * slot is negative or >= n_slots is skipped. Two active sequences must not share a slot, and S must
- * not overlap the pool.
+ * not overlap the pool. At most 2^30 - 1 (sequence, head) pairs a call, here and for gdn2_state_load.
  */
 GDN2_API gdn2_status gdn2_state_store(int n_seq, int h_v, int dk, int dv, gdn2_q8_format format,
                              const float* S, const int32_t* slots,
@@ -350,8 +350,8 @@ GDN2_API gdn2_status gdn2_state_commit_q8(int n_seq, int h_v, int dk, int dv, in
  * since the previous gdn2_device_status on this device in *flags, and clears them. It
  * synchronises `stream` (0 = the legacy default stream); work queued on other streams is
  * covered once it has completed.
- *   GDN2_DEVICE_WAIT_TIMEOUT  a bounded wait inside the tensor-core prefill or the
- *                             multi-token decode ran out (4 s): that CTA released its
+ *   GDN2_DEVICE_WAIT_TIMEOUT  a bounded wait inside the tensor-core prefill, the
+ *                             multi-token decode or the 8-bit decode ran out (4 s): that CTA released its
  *                             tensor memory (prefill) and returned without writing its rows
  *                             of o and its states, so the outputs of that call are
  *                             incomplete.
@@ -384,7 +384,7 @@ GDN2_API gdn2_status gdn2_device_status(unsigned int* flags, gdn2_stream_t strea
 
 /*
  * Testing only: the limit of the bounded waits of the tensor-core prefill and of the
- * multi-token decode for later calls from any thread (wait_ns = 0 restores the default of
+ * multi-token and 8-bit decodes for later calls from any thread (wait_ns = 0 restores the default of
  * 4 s), and, when withhold_first_load is non-zero, a prefill whose producer never issues its
  * first loads and a multi-token decode that never issues its first state load. With a short
  * limit the waits then run out, the kernel records GDN2_DEVICE_WAIT_TIMEOUT and returns,

@@ -98,6 +98,7 @@ def test_state_calls_reject_before_device_work(g):
     assert store(dk=96) == 2 and b"dk = 96" in _err(g)
     assert store(dv=256) == 2
     assert store(fmt=2) == 1 and b"8-bit format 2" in _err(g)
+    assert store(n=65535, h=32768, n_slots=65535) == 2 and b"above 2^30 - 1" in _err(g)
     assert store(n_slots=0) == 1
     assert store(slots=None, n_slots=1) == 1 and b"n_slots = 1 too small" in _err(g)
     assert store(S=None) == 1 and b"S is NULL" in _err(g)
