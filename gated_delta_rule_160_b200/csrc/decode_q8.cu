@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, 
             }
             // the new state, G rows at a time
             constexpr int kPasses = RW / G;
-#pragma unroll 1
+#pragma unroll  // the second pass's reads beside the first one's scales: 81.2 -> 79.9 us
             for (int ps_ = 0; ps_ < kPasses; ++ps_) {
                 const int i0 = (kPasses - 1 - ps_) * G;
 #pragma unroll
@@ -385,23 +385,27 @@ __global__ void __launch_bounds__(Cfg<DK, DV, kFmt, T, kPro, kOne>::NT, Cfg<DK, 
                         *reinterpret_cast<float4*>(&rv[5][i0 + 4 * i]) = make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
                 }
                 __syncwarp();
-                float scale = 0.f, inv = 1.f;
-                if (lane < G) {
-                    q8_scale<kFmt>(rv[5][i0 + lane], scale, inv);
-                    rv[5][i0 + lane] = inv;
+                float scale, inv;
+                q8_scale<kFmt>(rv[5][i0 + lane % G], scale, inv);
+                // (every lane takes a scale, some the same: a branch around it cost 1 %)
+                if (kOne) {
+                    __syncwarp();
+                    rv[5][i0 + lane % G] = inv;
+                    __syncwarp();
                 }
-                __syncwarp();
+                const auto inv_of = [&](int i) {  // of rows i and i + 1; kOne 80.0 us this way, 83 by shuffles, the other form 84.7 and 83.2
+                    return kOne ? *reinterpret_cast<const f32x2*>(&rv[5][i0 + i]) : pack2(__shfl_sync(0xffffffffu, inv, i), __shfl_sync(0xffffffffu, inv, i + 1));
+                };
                 const bool zero_rows = __any_sync(0xffffffffu, inv == 0.f);
                 uint32_t word[G];
 #pragma unroll
                 for (int i = 0; i < G / 4; ++i) {
-                    const ulonglong2 i4 = pairs(&rv[5][i0 + 4 * i]);
-                    q8_pack_pair<kFmt, CPL>(v[2 * i], i4.x, word[4 * i], word[4 * i + 1]);
-                    q8_pack_pair<kFmt, CPL>(v[2 * i + 1], i4.y, word[4 * i + 2], word[4 * i + 3]);
+                    q8_pack_pair<kFmt, CPL>(v[2 * i], inv_of(4 * i), word[4 * i], word[4 * i + 1]);
+                    q8_pack_pair<kFmt, CPL>(v[2 * i + 1], inv_of(4 * i + 2), word[4 * i + 2], word[4 * i + 3]);
                 }
                 if (zero_rows) {  // rows whose codes are 0 whatever they hold
 #pragma unroll
-                    for (int i = 0; i < G; ++i) word[i] = rv[5][i0 + i] == 0.f ? 0u : word[i];
+                    for (int i = 0; i < G; ++i) word[i] = (kOne ? rv[5][i0 + i] : __shfl_sync(0xffffffffu, inv, i)) == 0.f ? 0u : word[i];
                 }
                 auto put = [&](void* codes, float* sc, size_t state) {
                     const size_t r0 = state * DK + warp * RW + i0;
