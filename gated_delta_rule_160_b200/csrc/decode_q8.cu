@@ -18,11 +18,11 @@
 // arithmetic runs on pairs of rows: packed two-wide instructions take the rows' factors as they
 // lie in shared memory.
 //
-// Measured on B200, 256 sequences x 32 heads x 128 x 128, e4m3, one token: 83.0 us for 0.296 GB of
-// codes, scales and tokens (3.56 TB/s, 0.55 of the copy bandwidth; the fp32 pool takes 165 us). Not
-// HBM bounds it but the 6.1 K warp instructions of an item: unpacking, two sums, the update, the
-// magnitudes, rounding; 55 % of issue slots, fp32 pipe 41 %. 64 sequences, 4 tokens with the state
-// after each: 86.2 us.
+// Measured on B200, 256 sequences x 32 heads x 128 x 128, e4m3, one token: 80.4 us for 0.296 GB of
+// codes, scales and tokens (3.68 TB/s, 0.57 of the copy bandwidth; the fp32 pool takes 165 us). Not
+// HBM bounds it but the 5.6 K warp instructions of an item: unpacking, two sums, the update, the
+// magnitudes, rounding; more warps per SM do not help, and no pipe is full. 64 sequences, 4 tokens with
+// the state after each: 83.2 us.
 #include <algorithm>
 #include <atomic>
 

@@ -307,3 +307,48 @@ def test_states_and_keys_of_any_size(g, oracle_mod, fmt, steps, size):
         ref_o, ref_s = _oracle(oracle_mod, d, n, 1, torch.from_numpy(S0[n]))
         assert rel_err(o[n], ref_o) <= TOL32
         _check_written(codes[n], scales[n], ref_s, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n_tok,steps", [(1, False), (1, True), (8, False), (8, True)])
+@pytest.mark.parametrize("what", ["decay", "write", "key", "erase", "scale"])
+def test_factors_that_leave_the_ordinary_range(g, oracle_mod, fmt, n_tok, steps, what):
+    """Decays that erase in one token or over several, values of 1e12 and 1e30, keys of 1e8, erase gates of 4096,
+    scales from 1e-30 to 1e30, next to ordinary rows, tokens and columns."""
+    N = 2
+    d = _tokens(N, n_tok, 1, 2, 128, 64, torch.float32, seed=19)
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    S = 0.05 * torch.randn(N, 2, 128, 64, generator=gen, device="cuda")
+    if what == "decay":
+        d["log_alpha"][:, :, 0, ::3] = -30.0
+        d["log_alpha"][:, n_tok // 2, 1, 1::5] = float("-inf")
+        d["log_alpha"][:, :, 1, 2::7] = -9.0
+    elif what == "write":
+        d["v"][:, n_tok // 2, 0, 3] = 1e12
+        d["v"][:, -1, 1] *= 1e30
+    elif what == "key":
+        d["k"][:, n_tok // 2, 0, ::4] *= 1e8
+        d["b"][:] *= 1e-9  # (an erase along such a key would blow the state up)
+    elif what == "erase":
+        d["b"][:, 0, :, ::9] = 4096.0
+        d["k"][:] *= 1e-2
+    else:
+        S *= torch.logspace(-30, 30, 128, device="cuda")[torch.randperm(128, generator=gen, device="cuda")][:, None]
+        d["k"][:] *= 1e-3
+    c, sc = R.quantise(S.cpu().numpy(), fmt)
+    codes, scales = torch.from_numpy(c.astype(np.float32)).cuda().to(fmt), torch.from_numpy(sc).cuda()
+    S0 = R.read_back(codes, scales)
+    o, cs, ss = g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, want_steps=steps)
+    torch.cuda.synchronize()
+    heads = lambda x, h: x[:, h:h + 1] if x.shape[1] == 2 else x  # noqa: E731
+    for n in range(N):
+        for h in range(2):  # a head by itself: the bounds go by its own sizes
+            sl = {k_: heads(d[k_][n], h).cpu().contiguous() for k_ in NAMES}
+            for t in range(n_tok if steps else 0):
+                _, ref = oracle_mod.fwd_ref(*(sl[k_][:t + 1].contiguous() for k_ in NAMES), S0=torch.from_numpy(S0[n:n + 1, h:h + 1]), n_seq=1)
+                _check_written(cs[n, t, h], ss[n, t, h], ref[0, 0], fmt)
+            ref_o, ref = oracle_mod.fwd_ref(*(sl[k_] for k_ in NAMES), S0=torch.from_numpy(S0[n:n + 1, h:h + 1]), n_seq=1)
+            for t in range(n_tok):
+                assert rel_err(o[n, t, h], ref_o[t, 0]) <= TOL32
+            _check_written(codes[n, h], scales[n, h], ref[0, 0], fmt)
+    assert g.gdn2_device_status() == 0
