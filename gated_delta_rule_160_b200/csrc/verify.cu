@@ -9,13 +9,13 @@
 // Acceptance is decided in fp64 from the exact values of the inputs (u q is exact there: 24 + 24 bits).
 // Sums are good to 2^-48 relative, so over 131072 tokens the order of the additions shows in about one
 // draw of 10^9: differences p - q are rounded to fp32 and added in fp64, what the rounding took off is
-// exact in fp32 and added apart. (Both operands converted to fp64 cost 61 us where this takes 49.)
+// exact in fp32 and added apart. (Both operands converted to fp64 cost 61 us where this took 49.)
 //
 // The work is one row of p and one of q a sequence: HBM. A cluster of up to 8 CTAs shares a sequence: each
 // warp sums segments of 1024 weights with half a segment in flight, the CTAs exchange their sums
 // through distributed shared memory, and the CTA that holds the border scans its segment sums and then that
 // one segment again, out of L2. No workspace, no atomics on memory, one launch. Measured on B200: 256
-// sequences, 4 drafts, 131072 fp32 values a row: 49.4 us, 0.84 of what the rows take at the copy
+// sequences, 4 drafts, 131072 fp32 values a row: 48.0 us, 0.87 of what the rows take at the copy
 // bandwidth; one sequence, 3 drafts, 32768 values: 6.8 us, the latency of drafts, their
 // probabilities, the row and its segment again, one after the other.
 #include <cooperative_groups.h>
@@ -168,7 +168,7 @@ __device__ __forceinline__ uint4 load16(const T* x, const T* row, int V) {
                       __funnelshift_r(u[3], u[4], bits));
 }
 
-// This lane's share of one segment's sum, kSeg / 2 (values of 4 bytes) or more loaded before their first
+// This lane's share of one segment's sum (streaming loads: 47.9 us, 49.1 without), kSeg / 2 (values of 4 bytes) or more loaded before their first
 // use. Rows that start at 16-byte boundaries and hold whole vectors are read as such; others value by
 // value in 4 bytes, as shifted vectors in 2.
 template <typename T, bool kVec>
@@ -184,8 +184,8 @@ __device__ __forceinline__ double segment(const Row<T>& row, int j0, int V, int 
                 const int j = j1 + i * 32 * N;
                 pv[i] = qv[i] = make_uint4(0, 0, 0, 0);
                 if (j < V) {
-                    pv[i] = kVec ? __ldg(reinterpret_cast<const uint4*>(row.p + j)) : load16(row.p + j, row.p, V);
-                    if (row.mode == kResidual) qv[i] = kVec ? __ldg(reinterpret_cast<const uint4*>(row.q + j)) : load16(row.q + j, row.q, V);
+                    pv[i] = kVec ? __ldcs(reinterpret_cast<const uint4*>(row.p + j)) : load16(row.p + j, row.p, V);
+                    if (row.mode == kResidual) qv[i] = kVec ? __ldcs(reinterpret_cast<const uint4*>(row.q + j)) : load16(row.q + j, row.q, V);
                 }
             }
 #pragma unroll
