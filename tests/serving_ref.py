@@ -53,8 +53,10 @@ def half_step(S, dtype):
 
 
 def clean(x):
-    x = float(x)
-    return x if 0.0 < x < float("inf") else 0.0
+    """A probability, or a row of them, as it counts: 0 unless it is positive and finite."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore"):
+        return np.where((x > 0) & np.isfinite(x), x, 0.0)
 
 
 def verify(p, q, drafts, u, u_last, lens=None):
@@ -75,17 +77,17 @@ def verify(p, q, drafts, u, u_last, lens=None):
             if not 0 <= t < V:
                 break
             qt = 1.0 if q is None else clean(q[s, a, t])
-            if not float(u[s, a]) * qt < clean(p[s, a, t]):
+            if not float(u[s, a]) * float(qt) < float(clean(p[s, a, t])):
                 break
             a += 1
-        row = np.array([clean(x) for x in p[s, a]])
+        row = clean(p[s, a])
         if a < m:
             rest = row.copy()
             if q is None:
                 if 0 <= drafts[s, a] < V:
                     rest[drafts[s, a]] = 0.0
             else:
-                rest = np.maximum(row - np.array([clean(x) for x in q[s, a]]), 0.0)
+                rest = np.maximum(row - clean(q[s, a]), 0.0)
             row = rest if rest.sum() > 0 else row
         cum = np.cumsum(row)
         ul = float(u_last[s])

@@ -352,3 +352,22 @@ def test_factors_that_leave_the_ordinary_range(g, oracle_mod, fmt, n_tok, steps,
                 assert rel_err(o[n, t, h], ref_o[t, 0]) <= TOL32
             _check_written(codes[n, h], scales[n, h], ref[0, 0], fmt)
     assert g.gdn2_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n_tok", [1, 2])
+def test_most_sequences(g, fmt, n_tok):
+    """65535 sequences, nearly all idle: the active ones at both ends and in between as by themselves."""
+    N = 65535
+    live = [0, 1, 591, 592, 40000, 65533, 65534]
+    d = _tokens(N, n_tok, 1, 1, 64, 64, torch.bfloat16, seed=20)
+    codes, scales = _pool(len(live), 1, 64, 64, fmt, seed=20)
+    c0, s0 = codes.clone(), scales.clone()
+    slots = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    slots[live] = torch.arange(len(live), dtype=torch.int32, device="cuda")
+    o = torch.full((N, n_tok, 1, 64), 123.0, device="cuda")
+    g.gdn2_decode_multi_q8(*(d[k_] for k_ in NAMES), codes, scales, slots=slots, o=o)
+    o1, _, _ = g.gdn2_decode_multi_q8(*(d[k_][live].contiguous() for k_ in NAMES), c0, s0)
+    assert torch.equal(o[live], o1) and torch.equal(codes.view(torch.uint8), c0.view(torch.uint8)) and torch.equal(scales, s0)
+    o[live] = 123.0
+    assert torch.all(o == 123.0) and g.gdn2_device_status() == 0

@@ -68,7 +68,7 @@ def test_most_drafts(g):
         g.gdn2_verify_drafts(*_case(1, 32, 8, torch.float32, seed=3))
 
 
-@pytest.mark.parametrize("V", [130000, 262147, 1048576])
+@pytest.mark.parametrize("V", [130000, 262147, 1048576, 4194303, 4194304])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_large_vocabularies(g, V, dtype):
     """Every accepted length, the first and last tokens and both ends of the random number."""
@@ -78,6 +78,13 @@ def test_large_vocabularies(g, V, dtype):
     u[0] = u[3, 0] = 1.0
     u[1] = u[4] = 0.0
     _check(g, p, q, drafts, u, ul)
+
+
+def test_most_sequences(g):
+    N = 65535
+    p, q, drafts, u, ul = _case(N, 2, 9, torch.float32, seed=8)
+    lens = (torch.arange(N, device="cuda") % 4 - 1).to(torch.int32)
+    _check(g, p, q, drafts, u, ul, lens)
 
 
 def test_all_the_weight_in_one_place(g):
