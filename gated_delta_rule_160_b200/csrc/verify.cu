@@ -242,7 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
             const int t = drafts[lane];
             if (t >= 0 && t < V) {
                 const float pt = clean(to_f32(P[(size_t)lane * V + t])), qt = Q ? clean(to_f32(Q[(size_t)lane * V + t])) : 1.f;
-                yes = (double)a.u_accept[(size_t)n * k + lane] * (double)qt < (double)pt;
+                const float u = a.u_accept[(size_t)n * k + lane];
+                // below 0 as 0 (else a token without target probability would pass); a NaN stays one and refuses
+                yes = (u < 0.f ? 0.0 : (double)u) * (double)qt < (double)pt;
             }
         }
         const unsigned no = ~__ballot_sync(0xffffffffu, yes);  // lane m's bit is set: m <= 31

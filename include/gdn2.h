@@ -315,7 +315,9 @@ GDN2_API gdn2_status gdn2_decode_multi_q8_prologue(const gdn2_shape* shape, gdn2
  *   tokens int32 [n_seq, n_draft + 1]: the accepted tokens, the drawn one at place a, -1 behind
  *     it (all -1: inactive). The drawn token is -1 where p_a has no weight at all.
  * A probability that is negative, infinite or NaN counts as 0; a drafted token outside the vocabulary is
- * never accepted; a random number outside [0, 1] counts as the nearest bound, NaN as a refusal or 0.
+ * never accepted. u_accept below 0 counts as 0, so a token without target probability is never accepted;
+ * above 1 it enters the product as it is; NaN, or infinite at q_i(t_i) = 0, it refuses. u_sample outside
+ * [0, 1] counts as the nearest bound, NaN as 0.
  * Supported: n_draft 0..GDN2_VERIFY_MAX_DRAFTS, vocab 1..GDN2_VERIFY_MAX_VOCAB; any alignment of
  * the rows (pointers aligned to their elements).
  */
