@@ -7,9 +7,12 @@
 // CDF: the lowest j with r_0 + .. + r_j > u (r_0 + .. + r_{V-1}).
 //
 // Acceptance is decided in fp64 from the exact values of the inputs (u q is exact there: 24 + 24 bits).
-// Sums are good to 2^-48 relative, so over 131072 tokens the order of the additions shows in about one
-// draw of 10^9: differences p - q are rounded to fp32 and added in fp64, what the rounding took off is
-// exact in fp32 and added apart. (Both operands converted to fp64 cost 61 us where this took 49.)
+// A difference p - q is rounded to fp32 and added in fp64; what the rounding took off, at most 2^-24 of it, is exact in
+// fp32, is added there as a tree over 16 values (four roundings: 2^-46 of the weights) and then in fp64.
+// With the 100 fp64 additions at most on a value's way to the border (100 2^-53), sums are good to
+// 2^-45 of the weights in them; over 131072 tokens the order of the additions then shows in at most one draw of 10^7.
+// (256 rows of 131072 fp32 values: 48.5 us; the trees over 4 values only 50.5; both operands converted to
+// fp64 61; remainders added one by one over a segment 48.4, but good to 2^-43 only.)
 //
 // The work is one row of p and one of q a sequence: HBM. A cluster of up to 8 CTAs shares a sequence: each
 // warp sums segments of 1024 weights with half a segment in flight, the CTAs exchange their sums
@@ -90,18 +93,18 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
     return x;
 }
 
-// A sum of weights to about 2^-48 relative: the rounded differences in fp64, their errors (each below
-// 2^-24 of its difference) in fp32.
-struct Sum {
-    double hi = 0.0;
-    float lo = 0.f;
-    __device__ __forceinline__ double value() const { return hi + (double)lo; }
-};
+// The sum of N values as a balanced tree: log2 N roundings on each.
+template <int N>
+__device__ __forceinline__ float tree_sum(const float* x) {
+    if constexpr (N == 1) return x[0];
+    else return tree_sum<N / 2>(x) + tree_sum<N / 2>(x + N / 2);
+}
 
-// Add the weights of the N tokens j, j + kStep, ..; nearly all rows hold only finite values from 0 up, which one
-// comparison finds out for all N.
+// Add the weights of the N tokens j, j + kStep, .. to s and return the sum of what the differences among
+// them rounded off; nearly all rows hold only finite values from 0 up, which one comparison finds out for
+// all N.
 template <int N, int kStep = 1>
-__device__ __forceinline__ void add(Sum& s, float* p, float* q, int mode, int j, int t) {
+__device__ __forceinline__ float add(double& s, float* p, float* q, int mode, int j, int t) {
     uint32_t most = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) most = max(most, __float_as_uint(p[e]));
@@ -116,18 +119,20 @@ __device__ __forceinline__ void add(Sum& s, float* p, float* q, int mode, int j,
             q[e] = clean(q[e]);
         }
     }
-    if (mode == kResidual) {
+    if (mode != kResidual) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float m = fminf(p[e], q[e]);      // p - m = max(p - q, 0)
-            const float d = __fsub_rn(p[e], m);
-            s.lo += __fsub_rn(__fsub_rn(p[e], d), m);  // what d rounded off (p >= m >= 0: exact)
-            s.hi += (double)d;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s.hi += (double)(mode == kOneHot && j + e * kStep == t ? 0.f : p[e]);
+        for (int e = 0; e < N; ++e) s += (double)(mode == kOneHot && j + e * kStep == t ? 0.f : p[e]);
+        return 0.f;
     }
+    float lost[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float m = fminf(p[e], q[e]);         // p - m = max(p - q, 0)
+        const float d = __fsub_rn(p[e], m);
+        lost[e] = __fsub_rn(__fsub_rn(p[e], d), m);  // what d rounded off (p >= m >= 0: exact)
+        s += (double)d;
+    }
+    return tree_sum<N>(lost);
 }
 
 // 16 bytes at `at`, wherever the row (lo up to hi) starts: the two 16-byte blocks around them, shifted. A
@@ -173,12 +178,13 @@ __device__ __forceinline__ uint4 load16(const T* x, const T* row, int V) {
 // value in 4 bytes, as shifted vectors in 2.
 template <typename T, bool kVec>
 __device__ __forceinline__ double segment(const Row<T>& row, int j0, int V, int lane) {
-    Sum s;
+    double s = 0.0;
     if (kVec || sizeof(T) == 2) {
         constexpr int N = Vec<T>::kN, IT = kSeg / (32 * N) / 2;
 #pragma unroll 1
         for (int j1 = j0 + lane * N; j1 < j0 + kSeg; j1 += IT * 32 * N) {
             uint4 pv[IT], qv[IT];
+            float lost[IT];
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int j = j1 + i * 32 * N;
@@ -193,8 +199,9 @@ __device__ __forceinline__ double segment(const Row<T>& row, int j0, int V, int 
                 float pf[N], qf[N];
                 Vec<T>::get(pv[i], pf);
                 Vec<T>::get(qv[i], qf);
-                add<N>(s, pf, qf, row.mode, j1 + i * 32 * N, row.t);
+                lost[i] = add<N>(s, pf, qf, row.mode, j1 + i * 32 * N, row.t);
             }
+            if (row.mode == kResidual) s += (double)tree_sum<IT>(lost);
         }
     } else {
         constexpr int U = 16;
@@ -207,10 +214,11 @@ __device__ __forceinline__ double segment(const Row<T>& row, int j0, int V, int 
                 pf[i] = j < V ? to_f32(row.p[j]) : 0.f;
                 qf[i] = j < V && row.mode == kResidual ? to_f32(row.q[j]) : 0.f;
             }
-            add<U, 32>(s, pf, qf, row.mode, j1, row.t);
+            const float lost = add<U, 32>(s, pf, qf, row.mode, j1, row.t);
+            if (row.mode == kResidual) s += (double)lost;
         }
     }
-    return s.value();
+    return s;
 }
 
 template <typename T, bool kVec, int kThreads>

@@ -310,7 +310,7 @@ GDN2_API gdn2_status gdn2_decode_multi_q8_prologue(const gdn2_shape* shape, gdn2
  * replaced by a token of max(p_a - q_a, 0), or of p_a where that is zero everywhere; with a = m
  * accepted, one more token comes from p_m. A token is drawn from weights r (they need not sum to
  * 1) as the lowest j with r_0 + .. + r_j > u_sample (r_0 + .. + r_{vocab-1}); acceptance is decided
- * exactly, the sums are good to 2^-48.
+ * exactly, the sums are good to 2^-45 of the weights in them.
  *   n_accepted int32 [n_seq]: a (-1: inactive)
  *   tokens int32 [n_seq, n_draft + 1]: the accepted tokens, the drawn one at place a, -1 behind
  *     it (all -1: inactive). The drawn token is -1 where p_a has no weight at all.
