@@ -3,7 +3,7 @@
 This package is a thin binding over the C ABI declared in ``include/gdn2.h``, by ctypes and, for
 the operators around the state pool, by ``csrc/binding.cpp``; every step of the recurrence runs
 in the CUDA kernels of ``libgdn2.so``. PyTorch provides device memory and streams only. There is
-no CPU fallback: if a library is missing or fails to load, the functions below raise.
+no CPU fallback: if a library is missing or fails to load, the functions that need it raise.
 
     gdn2_chunk_fwd(q, k, v, log_alpha, b, w, S0=None, cu_seqlens=None, ...) -> (o, S_T)
         (prologue=True: raw projections in, the pre-processing fused)
@@ -70,8 +70,8 @@ _lib = _binding = None
 
 
 def load_library(path: str = LIB_PATH):
-    """Load libgdn2.so (built by ``python -m gated_delta_rule_160_b200.build``)."""
-    global _lib, _binding
+    """Load libgdn2.so (built by ``python -m gated_delta_rule_160_b200.build``), and the binding module if it is there."""
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -115,15 +115,23 @@ def load_library(path: str = LIB_PATH):
     lib.gdn2_last_error_string.restype = ctypes.c_char_p
     lib.gdn2_last_error_string.argtypes = []
     lib.gdn2_version.restype = ctypes.c_int
+    _lib = lib
+    with contextlib.suppress(ImportError):  # only the operators around the state pool need it, and raise without it
+        _load_binding()
+    return lib
+
+
+def _load_binding():
+    """The module of csrc/binding.cpp, bound to the library that is loaded."""
+    global _binding
     try:
         binding = importlib.import_module("._binding", __name__)
     except ImportError as e:
         raise ImportError(f"{e}; run `python -m gated_delta_rule_160_b200.build`") from e
-    binding.init(Gdn2Error, *(ctypes.cast(getattr(lib, name), vp).value for name in (
+    binding.init(Gdn2Error, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
         "gdn2_state_store", "gdn2_state_load", "gdn2_decode_multi_q8", "gdn2_decode_multi_q8_prologue",
         "gdn2_verify_drafts", "gdn2_state_commit", "gdn2_state_commit_q8", "gdn2_last_error_string")))
-    _lib, _binding = lib, binding
-    return lib
+    _binding = binding
 
 
 def _ptr(t):
@@ -392,6 +400,8 @@ def _bound():
     device current, allocates missing outputs on the call's stream and calls the library."""
     if _binding is None:
         load_library()
+    if _binding is None:
+        _load_binding()
     return _binding
 
 

@@ -1,0 +1,64 @@
+"""The two compiled files of the package are independent: what libgdn2.so serves by itself needs no binding
+module, in building and in loading. Everything here runs without a GPU."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PACKAGE = "gated_delta_rule_160_b200"
+
+
+@pytest.fixture(scope="module")
+def build():
+    from gated_delta_rule_160_b200 import build
+    build.build()
+    return build
+
+
+def _copy(tmp_path):
+    """The package with libgdn2.so, but without a binding module."""
+    to = tmp_path / PACKAGE
+    shutil.copytree(os.path.join(ROOT, PACKAGE), to, ignore=shutil.ignore_patterns("__pycache__", "csrc", "_binding*"))
+    return to
+
+
+def _run(where, code):
+    return subprocess.run([sys.executable, "-c", code], cwd=where, capture_output=True, text=True, timeout=300,
+                          env={**os.environ, "PYTHONPATH": str(where)})
+
+
+LOADS = f"""
+import torch
+import {PACKAGE} as g
+assert g.__file__.startswith({{where!r}}), g.__file__
+assert g.load_library().gdn2_version() >= 210
+x = torch.zeros(1, 1, 64)
+try:
+    g.gdn2_decode_step(x, x, x, x, x, x, torch.zeros(1, 1, 64, 64))
+except ValueError as e:  # the check of its own arguments
+    assert 'must be a CUDA tensor' in str(e), e
+else:
+    raise AssertionError('host tensors taken')
+for call in (lambda: g.gdn2_state_load(x, x), lambda: g.gdn2_verify_drafts(x, x, x, x, x)):
+    try:
+        call()
+    except ImportError as e:
+        assert 'python -m {PACKAGE}.build' in str(e), e
+    else:
+        raise AssertionError('called without a binding')
+print('fine')
+"""
+
+
+@pytest.mark.parametrize("damaged", [False, True])
+def test_older_functions_work_without_the_binding(build, tmp_path, damaged):
+    """Missing or not loadable: prefill, decode and backward still reach libgdn2.so; the serving operators raise, and
+    say what to run."""
+    to = _copy(tmp_path)
+    if damaged:
+        (to / os.path.basename(build.BINDING)).write_bytes(b"not a library")
+    r = _run(tmp_path, LOADS.format(where=str(tmp_path)))
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
