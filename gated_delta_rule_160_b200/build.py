@@ -70,8 +70,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force, verbose)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp"
@@ -81,6 +80,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)  # first: it needs no torch
+    build_binding(force, verbose)
     return LIB
 
 

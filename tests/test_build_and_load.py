@@ -62,3 +62,20 @@ def test_older_functions_work_without_the_binding(build, tmp_path, damaged):
         (to / os.path.basename(build.BINDING)).write_bytes(b"not a library")
     r = _run(tmp_path, LOADS.format(where=str(tmp_path)))
     assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
+
+
+def test_library_is_built_before_the_binding(build, tmp_path, monkeypatch):
+    """A torch that the binding cannot be compiled against still gets libgdn2.so, and the failure is raised."""
+    commands = []
+
+    def compiler(cmd, **kw):
+        commands.append(cmd[0])
+        if cmd[0] == "g++":
+            raise subprocess.CalledProcessError(1, cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libgdn2.so"))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    with pytest.raises(subprocess.CalledProcessError):
+        build.build(force=True)
+    assert os.path.exists(build.LIB) and commands == [build.nvcc(), "g++"]
