@@ -29,8 +29,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import importlib
+import importlib.util
 import os
+import sys
 
 import torch
 
@@ -124,10 +125,15 @@ def load_library(path: str = LIB_PATH):
 def _load_binding():
     """The module of csrc/binding.cpp, bound to the library that is loaded."""
     global _binding
+    from .build import binding_path
+    name, path = __name__ + "._binding", binding_path()
+    spec = importlib.util.spec_from_file_location(name, path)
     try:
-        binding = importlib.import_module("._binding", __name__)
+        binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(binding)
     except ImportError as e:
-        raise ImportError(f"{e}; run `python -m gated_delta_rule_160_b200.build`") from e
+        raise ImportError(f"{path}: {e}; run `python -m gated_delta_rule_160_b200.build`") from e
+    sys.modules[name] = binding
     binding.init(Gdn2Error, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
         "gdn2_state_store", "gdn2_state_load", "gdn2_decode_multi_q8", "gdn2_decode_multi_q8_prologue",
         "gdn2_verify_drafts", "gdn2_state_commit", "gdn2_state_commit_q8", "gdn2_last_error_string")))

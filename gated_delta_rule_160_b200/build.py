@@ -1,5 +1,5 @@
-"""Build libgdn2.so (the sm_100a CUDA library) in-tree with nvcc, and _binding.so (the host-side
-binding of the serving operators, against the installed torch) with g++.
+"""Build libgdn2.so (the sm_100a CUDA library) in-tree with nvcc, and the host-side binding of the serving
+operators, against the installed torch, with g++.
 
 Usage: ``python -m gated_delta_rule_160_b200.build [--force]``. Both are written next
 to this file so that they travel with the source tree.
@@ -10,13 +10,25 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn2.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING = os.path.join(HERE, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+
+
+def binding_path() -> str:
+    """The binding module for the running torch and Python. It inlines their object layouts, so each version of
+    either has a file of its own: a module built against another one is neither taken for up to date nor loaded."""
+    torch_tag = f"torch{torch.__version__}-{(torch.version.git_version or '')[:8]}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_binding.{torch_tag}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+BINDING = binding_path()
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,16 +59,15 @@ def nvcc() -> str:
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """_binding.so: C++ over torch's headers, no CUDA code."""
-    import sysconfig
-
-    import torch
-    deps = [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return BINDING
+    """The binding module: C++ over torch's headers, no CUDA code. Built anew when its source, the headers or the
+    command here are newer."""
+    path = binding_path()
+    deps = [BINDING_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
-    tmp = BINDING + ".tmp"
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
@@ -66,8 +77,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -84,7 +95,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_library(force, verbose)  # first: it needs no torch
+    build_library(force, verbose)  # first: it needs nothing of torch's
     build_binding(force, verbose)
     return LIB
 

@@ -79,3 +79,49 @@ def test_library_is_built_before_the_binding(build, tmp_path, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         build.build(force=True)
     assert os.path.exists(build.LIB) and commands == [build.nvcc(), "g++"]
+
+
+def test_binding_belongs_to_one_torch_and_python(build, monkeypatch):
+    """The module inlines torch's and Python's object layouts: another version of either has another file, and an
+    existing file of the old one is not taken for it."""
+    import sysconfig
+
+    import torch
+    here = build.binding_path()
+    assert here == build.BINDING and os.path.exists(here) and os.path.dirname(here) == build.HERE
+    seen = {here}
+    soabi = sysconfig.get_config_var("SOABI")
+    for change in (lambda m: m.setattr(torch, "__version__", "99.1.0+cu1"), lambda m: m.setattr(torch.version, "git_version", "0" * 40),
+                   lambda m: m.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI),
+                   lambda m: m.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-x" if name == "SOABI" else None)):
+        with monkeypatch.context() as m:
+            change(m)
+            path = build.binding_path()
+            assert path not in seen and not os.path.exists(path)
+            seen.add(path)
+            commands = []
+            m.setattr(build.subprocess, "run", lambda cmd, **kw: (commands.append(cmd), open(cmd[cmd.index("-o") + 1], "w").close()))
+            m.setattr(build.os, "replace", lambda a, b: (os.remove(a), commands.append(b)))
+            assert build.build_binding() == path and len(commands) == 2 and commands[1] == path
+    assert sysconfig.get_config_var("SOABI") == soabi and build.binding_path() == here
+
+
+def test_binding_is_rebuilt_when_its_command_may_have_changed(build, monkeypatch):
+    """The flags stand in build.py: a newer one builds again."""
+    commands = []
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: commands.append(cmd))
+    monkeypatch.setattr(build.os, "replace", lambda a, b: None)
+    build.build_binding()
+    assert not commands
+    newer = os.path.getmtime(build.BINDING) + 10
+    real = os.path.getmtime
+    monkeypatch.setattr(build.os.path, "getmtime", lambda p: newer if os.path.basename(p) == "build.py" else real(p))
+    build.build_binding()
+    assert len(commands) == 1
+
+
+def test_a_binding_of_another_torch_is_not_loaded(build, tmp_path):
+    to = _copy(tmp_path)
+    shutil.copy(build.BINDING, to / os.path.basename(build.BINDING).replace("torch", "torch-0.0.0-"))
+    r = _run(tmp_path, LOADS.format(where=str(tmp_path)))
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
