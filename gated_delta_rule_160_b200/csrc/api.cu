@@ -252,6 +252,10 @@ gdn2_status check_serving(const gdn2_shape* shape, int n_tok, const int32_t* slo
     if (n_slots < 1 || (!slots && n_slots < shape->n_seq))
         return fail(GDN2_ERR_INVALID_ARG, "n_slots = %d too small (n_seq = %d, slots %s)", n_slots, shape->n_seq,
                     slots ? "given" : "NULL");
+    // the kernels go from pair to pair by adding their grid (a few CTAs per SM) in 32 bits
+    if ((long long)shape->n_seq * shape->h_v > 0x7fffffffLL - 0xffff)
+        return fail(GDN2_ERR_UNSUPPORTED, "n_seq * h_v = %lld (sequence, head) pairs above 2^31 - 2^16",
+                    (long long)shape->n_seq * shape->h_v);
     return GDN2_OK;
 }
 
