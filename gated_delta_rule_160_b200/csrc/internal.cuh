@@ -52,11 +52,14 @@ constexpr unsigned int kStatusDecayRange = GDN2_DEVICE_DECAY_RANGE;
 constexpr unsigned long long kDefaultWaitNs = 4000000000ull;
 
 // Pieces of the fused pre-processing, in fp32, on the special-function unit. Their errors
-// are absolute ~1e-7 (softplus: summed into log-decays) and relative ~1e-6 (sigmoid), far
-// below what the bf16 operands of the recurrence carry.
+// are absolute ~1e-7 (softplus: summed into log-decays) and relative ~1e-6 (sigmoid; the
+// exponential's is up to (2 + 1.2 |x|) 2^-23), far below what the bf16 operands of the
+// recurrence carry. With expf and the rounded quotient the 8-bit decode of 256 x 32 raw
+// tokens takes 88.0 us instead of 84.0, four tokens with per-token states 101.9 instead of 94.
 __device__ __forceinline__ float sigmoid_f(float x) {
-    // 1 / (1 + e^-x); the exponent is capped where the quotient is already ~1e-35
-    return __fdividef(1.f, 1.f + __expf(fminf(-x, 80.f)));
+    // 1 / (1 + e^-x): a NaN stays one, and where e^-x leaves the range the quotient is 0 (__fdividef gives
+    // that for divisors above 2^126 and for infinity)
+    return __fdividef(1.f, 1.f + __expf(-x));
 }
 __device__ __forceinline__ float softplus_f(float x) {  // log(1 + e^x), without overflow
     return fmaxf(x, 0.f) + __logf(1.f + __expf(-fabsf(x)));

@@ -289,7 +289,10 @@ GDN2_API gdn2_status gdn2_decode_multi_q8(const gdn2_shape* shape, gdn2_q8_forma
                                  void* codes, float* scales, int n_slots, void* o,
                                  void* code_steps, float* scale_steps, gdn2_stream_t stream);
 
-/* gdn2_decode_multi_q8 with the pre-processing of gdn2_chunk_fwd_prologue fused in. */
+/*
+ * gdn2_decode_multi_q8 with the pre-processing of gdn2_chunk_fwd_prologue fused in. Decay and gates
+ * are fp32 with a relative error of about 1e-6, up to (2 + 1.2 |x|) 2^-23 at a pre-activation x.
+ */
 GDN2_API gdn2_status gdn2_decode_multi_q8_prologue(const gdn2_shape* shape, gdn2_q8_format format, int n_tok,
                                           const int32_t* slots, const int32_t* slots_out,
                                           const void* q_raw, const void* k_raw, const void* v,
