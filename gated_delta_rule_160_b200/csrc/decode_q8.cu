@@ -18,11 +18,16 @@
 // arithmetic runs on pairs of rows: packed two-wide instructions take the rows' factors as they
 // lie in shared memory.
 //
-// Measured on B200, 256 sequences x 32 heads x 128 x 128, e4m3, one token: 80.4 us for 0.296 GB of
-// codes, scales and tokens (3.68 TB/s, 0.57 of the copy bandwidth; the fp32 pool takes 165 us). Not
-// HBM bounds it but the 5.6 K warp instructions of an item: unpacking, two sums, the update, the
-// magnitudes, rounding; more warps per SM do not help, and no pipe is full. 64 sequences, 4 tokens with
-// the state after each: 83.2 us.
+// Measured on B200, 256 sequences x 32 heads x 128 x 128, e4m3, one token: 80.3 us for 0.296 GB of
+// codes, scales and tokens (3.68 TB/s, 0.57 of the copy bandwidth; the fp32 pool takes 165 us). int8
+// 81.0, from raw projections 84.0 and 84.2. Neither HBM nor the issue of instructions bounds it: the
+// 5.6 K warp instructions of an item would take half of that at full rate, and 9 % fewer of them were
+// no faster. It is latency. An item is one chain of factors, sums, barrier, update, magnitudes, scales
+// and rounding; 4 warps a scheduler fill 52 % of its issue slots, the first stall is the barrier, and
+// more warps per SM (fewer registers each) did not help. 64 sequences, 4 tokens: with the state after
+// each 83.4 us (floor 35.1; int8 84.5, raw 93.9), without 64.5 (floor 13.6; int8 65.6, raw 75.9), by
+// the same chain a token. The 128 x 128 forms for several raw tokens spill 8 to 16 bytes at 128
+// registers.
 #include <algorithm>
 #include <atomic>
 

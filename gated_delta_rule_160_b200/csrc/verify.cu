@@ -7,20 +7,26 @@
 // CDF: the lowest j with r_0 + .. + r_j > u (r_0 + .. + r_{V-1}).
 //
 // Acceptance is decided in fp64 from the exact values of the inputs (u q is exact there: 24 + 24 bits).
-// A difference p - q is rounded to fp32 and added in fp64; what the rounding took off, at most 2^-24 of it, is exact in
-// fp32, is added there as a tree over 16 values (four roundings: 2^-46 of the weights) and then in fp64.
-// With the 100 fp64 additions at most on a value's way to the border (100 2^-53), sums are good to
-// 2^-45 of the weights in them; over 131072 tokens the order of the additions then shows in at most one draw of 10^7.
-// (256 rows of 131072 fp32 values: 48.5 us; the trees over 4 values only 50.5; both operands converted to
-// fp64 61; remainders added one by one over a segment 48.4, but good to 2^-43 only.)
+// A difference p - q is rounded to fp32 and added in fp64; what the rounding took off, at most 2^-24 of
+// it, is exact in fp32, is added there as a tree over 16 values (four roundings: 2^-46 of the weights)
+// and then in fp64. With the 100 fp64 additions at most on a value's way to the border (100 2^-53),
+// sums are good to 2^-45 of the weights in them; over 131072 tokens the order of the additions then
+// shows in at most one draw of 10^7. (256 rows of 131072 fp32 values: 48.5 us; the trees over 4 values
+// only 50.5; both operands converted to fp64 61; remainders added one by one over a segment 48.4, but
+// good to 2^-43 only.)
 //
-// The work is one row of p and one of q a sequence: HBM. A cluster of up to 8 CTAs shares a sequence: each
-// warp sums segments of 1024 weights with half a segment in flight, the CTAs exchange their sums
-// through distributed shared memory, and the CTA that holds the border scans its segment sums and then that
-// one segment again, out of L2. No workspace, no atomics on memory, one launch. Measured on B200: 256
-// sequences, 4 drafts, 131072 fp32 values a row: 48.0 us, 0.87 of what the rows take at the copy
-// bandwidth; one sequence, 3 drafts, 32768 values: 6.8 us, the latency of drafts, their
-// probabilities, the row and its segment again, one after the other.
+// The work is one row of p and, where a draft was refused, one of q a sequence. A cluster of up to 8
+// CTAs shares a sequence: each warp sums segments of 1024 weights with half a segment in flight, the
+// CTAs exchange their sums through distributed shared memory, and the CTA that holds the border scans
+// its segment sums and then that one segment again, out of L2. No workspace, no atomics on memory, one
+// launch. Measured on B200, 256 sequences, 4 drafts, 131072 values a row, 1.87 rows read a sequence:
+// fp32 48.4 us, 0.80 of the copy bandwidth, bound by HBM and by the accept phase of each cluster; bf16
+// 36.0 us, 0.54: half the bytes, but as many instructions (10.5 M warp instructions for 128 rows, 10.8
+// M in fp32: a minimum, three subtractions, two additions and a conversion a value). They take 18 us of
+// the 36 at full rate; 55 % of issue slots are used, and what waits waits for loads. Certain drafts,
+// which read p alone: 38.9 us in fp32 (0.53), 36.3 in bf16 (0.29). Rows that do not start at 16-byte
+// boundaries: 56.5 and 62.9 us. One sequence, 3 drafts, 32768 values: 6.5 us, the latency of drafts,
+// their probabilities, the row and its segment again, one after the other.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -388,10 +394,13 @@ cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t st) {
 
 template <typename T, bool kVec>
 cudaError_t launch_v(const VerifyArgs& a, cudaStream_t st) {
-    // CTAs of 4 warps where they fill the GPU (short CTAs overlap one sequence's loads with another's
-    // exchange), of 8 where they do not: 256 rows of 131072 fp32 values 48.8 us against 53.4, 64 rows of
-    // 131072 bf16 values 15.2 us against 13.2. In the cluster one segment for each warp, as far as
-    // 8 CTAs go.
+    // CTAs of 4 warps for large batches, of 8 for small ones; in the cluster one segment for each warp, as far
+    // as 8 CTAs go. 74 clusters of 8 x 8 warps are resident at a time, and up to there more warps a
+    // sequence win: 64 rows of 131072 values 15.1 us against 17.7 (fp32) and 13.5 against 15.6 (bf16). Beyond, the
+    // shorter CTAs overlap one sequence's loads with another's exchange: 128 rows 24.9 against 27.3 and 20.2
+    // against 23.5, 256 rows 45.0 against 49.1 and 36.2 against 43.1. With 32768 values or fewer the two are
+    // within 5 % of each other. The rule changes over at 128 rows (32 segments or more); 96 rows, on
+    // the 8-warp side, take 23.9 us where the other takes 21.4.
     const int segs = (a.vocab + kSeg - 1) / kSeg;
     const bool full = (long long)a.n_seq * std::min(segs, kMaxCluster * 4) >= 4096;
     int ctas = 1;

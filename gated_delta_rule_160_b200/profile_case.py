@@ -9,6 +9,7 @@
     python -m gated_delta_rule_160_b200.profile_case --kernel q8 --n-seq 128 --iters 3
     python -m gated_delta_rule_160_b200.profile_case --kernel q8_drafts --n-seq 64 --iters 3
     python -m gated_delta_rule_160_b200.profile_case --kernel verify --n-seq 128 --iters 3
+    python -m gated_delta_rule_160_b200.profile_case --kernel verify_bf16 --n-seq 128 --iters 3
 
 ``chunk`` runs gdn2_chunk_fwd on the first ``n-seq`` sequences of the 16-head, T=4096,
 d=128 bf16 prefill workload (2 sequences: 268 MB of inputs, larger than L2; ``T`` cuts them);
@@ -22,7 +23,7 @@ shared by 32 value heads, with an initial state), its sequences cut to ``T`` tok
 32-head decode workload whose states sit at seeded-random slots of a pool twice as large; ``q8``
 runs gdn2_decode_multi_q8 (e4m3 codes, one token) on ``n-seq`` sequences of that workload, and
 ``q8_drafts`` the same with 4 tokens and the state after each; ``verify`` runs gdn2_verify_drafts on
-``n-seq`` sequences of 4 drafts over 131072 tokens. Each
+``n-seq`` sequences of 4 drafts over 131072 tokens, and ``verify_bf16`` the same in bf16. Each
 kernel is launched ``iters`` times; profile the last launches (ncu -s / -c).
 """
 import argparse
@@ -35,7 +36,7 @@ from gated_delta_rule_160_b200 import workloads as W
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--kernel", choices=["chunk", "prologue", "decode", "bwd", "grouped", "serving", "q8", "q8_drafts", "verify"],
+    ap.add_argument("--kernel", choices=["chunk", "prologue", "decode", "bwd", "grouped", "serving", "q8", "q8_drafts", "verify", "verify_bf16"],
                     default="chunk")
     ap.add_argument("--n-seq", type=int, default=2)
     ap.add_argument("--T", type=int, default=None, help="tokens per sequence (chunk, bwd, grouped)")
@@ -102,12 +103,13 @@ def main():
                          scale_steps=torch.zeros((N, n_tok) + scales.shape[1:], device="cuda"))
         for _ in range(a.iters):
             G.gdn2_decode_multi_q8(*(x[k] for k in ("q", "k", "v", "log_alpha", "b", "w")), codes, scales, **steps)
-    elif a.kernel == "verify":
+    elif a.kernel in ("verify", "verify_bf16"):
         N, n, V = a.n_seq, 4, 131072
         gen = torch.Generator(device="cuda").manual_seed(5)
         logits = 3 * torch.randn(N, n + 1, V, generator=gen, device="cuda")
         near = 0.9 * logits[:, :n] + torch.randn(N, n, V, generator=gen, device="cuda")
-        args = (torch.softmax(logits, -1), torch.softmax(near, -1), near.argmax(-1).to(torch.int32),
+        dt = torch.bfloat16 if a.kernel == "verify_bf16" else torch.float32
+        args = (torch.softmax(logits, -1).to(dt), torch.softmax(near, -1).to(dt), near.argmax(-1).to(torch.int32),
                 torch.rand(N, n, generator=gen, device="cuda"), torch.rand(N, generator=gen, device="cuda"))
         for _ in range(a.iters):
             G.gdn2_verify_drafts(*args)
