@@ -97,8 +97,9 @@ GDN2_API size_t gdn2_chunk_fwd_workspace_size(const gdn2_shape* shape, int varle
  * S0 == NULL starts every sequence from a zero state. S_T == NULL skips the final state.
  * S_T may be S0 itself (the states are then updated in place); no other output may overlap
  * an input. A zero-length sequence writes S_T = S0 (or 0) and no output.
- * A NaN in a token (raw gates of gdn2_chunk_fwd_prologue among them) shows in all that follows it in
- * its sequence, and with the tensor cores in the rows of o before it in its 64-token chunk too.
+ * A NaN in a token's k, v, decay or gates (raw ones of gdn2_chunk_fwd_prologue too) shows in the states and
+ * outputs that the recurrence carries it to, and on the tensor cores in the same columns of o for the
+ * tokens before it in its 64-token chunk.
  * workspace: device memory of at least gdn2_chunk_fwd_workspace_size() bytes, 256-byte
  * aligned, owned by the caller, reused freely after the call's work completes; may be
  * NULL when that size is 0.
